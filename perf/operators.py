@@ -174,15 +174,17 @@ def prepare(case, seed):
         return st
     V = case["V"]
     x = torch.randn((T, V), generator=g, device="cuda") * 2.0
-    # a few likely continuations stand out at every position
-    likely = torch.randint(0, V, (T, 24), generator=g, device="cuda")
+    # a few likely continuations stand out at every position (distinct ids: one in each 24th of those in use)
+    used = V - V // 1024
+    part = used // 24
+    likely = torch.randint(0, part, (T, 24), generator=g, device="cuda") + part * torch.arange(24, device="cuda")
     x.scatter_(1, likely, 4.0 + 9.0 * torch.rand((T, 24), generator=g, device="cuda"))
-    x[:, V - V // 1024:] = -math.inf                     # ids that the tokenizer does not use
+    x[:, used:] = -math.inf                              # ids that the tokenizer does not use
     st["logits"] = x.to(_TYPES[case["dtype"]])
     # sampled continuations, now and then an unlikely one, and prompt positions without a target
-    target = likely[:, 0].clone()
+    target = likely.gather(1, torch.randint(0, 24, (T, 1), generator=g, device="cuda")).squeeze(1)
     u = torch.rand((T,), generator=g, device="cuda")
-    anywhere = torch.randint(0, V - V // 1024, (T,), generator=g, device="cuda")
+    anywhere = torch.randint(0, used, (T,), generator=g, device="cuda")
     target = torch.where(u < 0.25, anywhere, target)
     st["targets"] = torch.where(u > 0.95, torch.full_like(target, IGNORED), target)
     if op == "logprobs_grad":
