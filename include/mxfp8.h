@@ -746,4 +746,7 @@ const char *mxfp8_version(void);
 }
 #endif
 
+/* routing, expert rows and token log-probabilities */
+#include "mxfp8_tokens.h"
+
 #endif /* MXFP8_H */

@@ -927,3 +927,13 @@ def selfcheck_rel_err(w_q: torch.Tensor, w_s: torch.Tensor, packed: PackedWeight
     torch.cuda.current_stream(dev).synchronize()
     r = res.cpu().tolist()
     return r[0], r[1], r[2]
+
+
+# ------------------------------------------------------------------ token-level operators
+
+from .logprobs import TokenLogprobs, token_logprobs, token_logprobs_backward  # noqa: E402
+from .moe import (RouteTables, moe_combine, moe_combine_backward, route, route_backward,  # noqa: E402
+                  route_rows, route_tables)
+
+__all__ += ["route", "route_backward", "route_rows", "route_tables", "RouteTables", "moe_combine",
+            "moe_combine_backward", "token_logprobs", "token_logprobs_backward", "TokenLogprobs"]

@@ -7,6 +7,7 @@
 #include <mutex>
 #include <string.h>
 
+#include "mx_api.hpp"
 #include "mx_launch.hpp"
 
 namespace mx {
@@ -49,29 +50,6 @@ int device_arch_ok() {
     return d->gfx950 ? 1 : 0;
 }
 
-}  // namespace mx
-
-using namespace mx;
-
-namespace {
-
-constexpr int64_t kMaxDim = (int64_t)1 << 31;     // any single dimension
-constexpr int64_t kMaxK = (int64_t)1 << 22;       // 256 rows x K must stay < 2^31 B
-constexpr int64_t kMaxSelfcheckRows = 4096;       // probe rows of a self-check
-
-bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
-
-// The integer a caller passed for an enum parameter.  C callers may pass any
-// int; reading such a value through the enum type is undefined in C++ (the
-// host UBSan build flags it), so enum arguments are validated on their bytes.
-template <class E>
-int raw(const E &e) {
-    static_assert(sizeof(E) == sizeof(int), "enum arguments are int-sized");
-    int v = 0;
-    memcpy(&v, &e, sizeof v);
-    return v;
-}
-
 mxfp8_status check_device() {
     int dev = 0;
     const hipError_t e = hipGetDevice(&dev);
@@ -91,6 +69,18 @@ mxfp8_status finish(hipError_t e) {
     }
     return MXFP8_OK;
 }
+
+}  // namespace mx
+
+using namespace mx;
+
+namespace {
+
+constexpr int64_t kMaxDim = (int64_t)1 << 31;     // any single dimension
+constexpr int64_t kMaxK = (int64_t)1 << 22;       // 256 rows x K must stay < 2^31 B
+constexpr int64_t kMaxSelfcheckRows = 4096;       // probe rows of a self-check
+
+bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
 
 // the axis-0 and dual quantizers run one workgroup per 128x128 tile on a
 // one-dimensional grid

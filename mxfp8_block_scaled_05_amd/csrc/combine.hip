@@ -1,0 +1,134 @@
+// Expert rows back in token order (the weighted sum of a token's experts) and
+// the gradients of that sum.
+#include "mx_launch.hpp"
+#include "mx_wave.hpp"
+
+namespace mx {
+
+namespace {
+
+constexpr int kBlock = 256;
+
+// One 16-byte piece of a row: all of it, or its first n elements.
+template <class E>
+__device__ __forceinline__ void load_piece(const E *p, int n, float *f) {
+    constexpr int kV = Elem<E>::kVec;
+    if (n >= kV) {
+        Elem<E>::unpack(load16(p), f);
+    } else {
+#pragma unroll
+        for (int i = 0; i < kV; ++i) f[i] = i < n ? Elem<E>::get(p[i]) : 0.0f;
+    }
+}
+template <class E>
+__device__ __forceinline__ void store_piece(E *p, int n, const float *f) {
+    constexpr int kV = Elem<E>::kVec;
+    if (n >= kV) {
+        store16(p, Elem<E>::pack(f));
+    } else {
+#pragma unroll
+        for (int i = 0; i < kV; ++i)
+            if (i < n) p[i] = Elem<E>::put(f[i]);
+    }
+}
+
+// out[t] = sum_j w[t][j] y[pair_row[t][j]], in fp32 and in the order of j,
+// rounded once.  HBM-bound: every chosen row is read once.  A thread holds
+// one 16-byte piece of one token.
+template <class E>
+__global__ __launch_bounds__(kBlock) void combine_kernel(const CombineArgs a, int64_t pieces) {
+    constexpr int kV = Elem<E>::kVec;
+    const int64_t i = (int64_t)blockIdx.x * kBlock + threadIdx.x;
+    const int64_t t = i / pieces;
+    if (t >= a.T) return;
+    const int64_t col = (i - t * pieces) * kV;
+    const int n = (int)(a.H - col < kV ? a.H - col : kV);
+    const E *y = static_cast<const E *>(a.y) + col;
+    float acc[kV];
+#pragma unroll
+    for (int e = 0; e < kV; ++e) acc[e] = 0.0f;
+    for (int j = 0; j < a.k; ++j) {
+        const int row = a.pair_row[t * a.k + j];
+        const float w = a.w[t * a.k + j];
+        if (row < 0 || row >= a.rows) continue;
+        float f[kV];
+        load_piece(y + row * a.H, n, f);
+#pragma unroll
+        for (int e = 0; e < kV; ++e) acc[e] = __builtin_fmaf(w, f[e], acc[e]);
+    }
+    store_piece(static_cast<E *>(a.out) + t * a.H + col, n, acc);
+}
+
+// A wave per (token, choice): d_y[row] = w d_out[t] and d_w = <d_out[t],
+// y[row]>, the token's d_out row read by the neighbouring waves of the block
+// from the cache.  The blocks after those zero the rows no token owns.
+template <class E>
+__global__ __launch_bounds__(kBlock) void combine_backward_kernel(const CombineArgs a, int64_t pair_blocks) {
+    constexpr int kV = Elem<E>::kVec;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    E *d_y = static_cast<E *>(a.d_y);
+    if ((int64_t)blockIdx.x < pair_blocks) {
+        const int64_t p = (int64_t)blockIdx.x * (kBlock / 64) + wave;
+        if (p >= a.T * a.k) return;
+        const int64_t t = p / a.k;
+        const int64_t row = a.pair_row[p];
+        const float w = a.w[p];
+        const bool real = row >= 0 && row < a.rows;
+        float dot = 0.0f;
+        if (real) {
+            const E *d = static_cast<const E *>(a.d_out) + t * a.H;
+            const E *y = static_cast<const E *>(a.y) + row * a.H;
+            for (int64_t col = lane * kV; col < a.H; col += 64 * kV) {
+                const int n = (int)(a.H - col < kV ? a.H - col : kV);
+                float g[kV], f[kV];
+                load_piece(d + col, n, g);
+                load_piece(y + col, n, f);
+#pragma unroll
+                for (int e = 0; e < kV; ++e) {
+                    dot = __builtin_fmaf(g[e], f[e], dot);
+                    g[e] *= w;
+                }
+                store_piece(d_y + row * a.H + col, n, g);
+            }
+        }
+        dot = group_reduce<64>(dot, OpAdd());
+        if (lane == 0) a.d_w[p] = dot;
+        return;
+    }
+    const int64_t base = (((int64_t)blockIdx.x - pair_blocks) * (kBlock / 64) + wave) * 64;
+    if (base >= a.rows) return;
+    const int64_t mine = base + lane;
+    bool empty = false;
+    if (mine < a.rows) {
+        const int64_t t = a.row_token[mine];
+        empty = t < 0 || t >= a.T;
+    }
+    float zero[kV];
+#pragma unroll
+    for (int e = 0; e < kV; ++e) zero[e] = 0.0f;
+    for (uint64_t m = __ballot(empty); m; m &= m - 1) {
+        const int64_t row = base + __builtin_ctzll(m);
+        for (int64_t col = lane * kV; col < a.H; col += 64 * kV)
+            store_piece(d_y + row * a.H + col, (int)(a.H - col < kV ? a.H - col : kV), zero);
+    }
+}
+
+}  // namespace
+
+hipError_t launch_combine(const CombineArgs &a, bool bf16, hipStream_t stream) {
+    const int64_t pieces = ceil_div(a.H, bf16 ? 8 : 4);
+    const unsigned grid = (unsigned)ceil_div(a.T * pieces, kBlock);
+    if (bf16) combine_kernel<uint16_t><<<grid, kBlock, 0, stream>>>(a, pieces);
+    else combine_kernel<float><<<grid, kBlock, 0, stream>>>(a, pieces);
+    return hipGetLastError();
+}
+
+hipError_t launch_combine_backward(const CombineArgs &a, bool bf16, hipStream_t stream) {
+    const int64_t pair_blocks = ceil_div(a.T * a.k, kBlock / 64);
+    const unsigned grid = (unsigned)(pair_blocks + ceil_div(a.rows, kBlock));
+    if (bf16) combine_backward_kernel<uint16_t><<<grid, kBlock, 0, stream>>>(a, pair_blocks);
+    else combine_backward_kernel<float><<<grid, kBlock, 0, stream>>>(a, pair_blocks);
+    return hipGetLastError();
+}
+
+}  // namespace mx

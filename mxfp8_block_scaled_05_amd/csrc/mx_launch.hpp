@@ -167,6 +167,85 @@ hipError_t launch_grouped_gemm_wgrad(const uint8_t *a_q, const uint8_t *a_s, con
                                      int64_t T, int64_t M, int64_t N, void *c, bool c_bf16,
                                      hipStream_t stream);
 
+// Expert routing (route.hip).  T >= 1 rows of E logits, ld elements apart.
+constexpr int kRouteMaxExperts = 512;
+constexpr int kRouteMaxK = 32;
+constexpr int kRouteMaxGroups = 64;
+struct RouteArgs {
+    const void *x;              // logits [T][ld]
+    int64_t ld, T;
+    const float *bias;          // [E] or null
+    int32_t *ids;               // [T][k] (read by the backward)
+    float *w;                   // [T][k]
+    const float *dw;            // [T][k], backward only
+    void *dx;                   // [T][E], backward only
+    float scale;
+    int E, k, groups, size, kept, group_top;   // size = E / groups
+    bool sigmoid, renorm;
+    // set by the launchers
+    bool order_x, order_exact;
+    int lanes_shift, candidates;
+};
+hipError_t launch_route(const RouteArgs &a, bool bf16, hipStream_t stream);
+hipError_t launch_route_backward(const RouteArgs &a, bool bf16, hipStream_t stream);
+
+// Row tables (tables.hip).  pairs >= 1; hist: chunks * E ints when a batch
+// takes more than one chunk (route_tables_workspace).
+constexpr int kTablesMaxExperts = 1024;
+constexpr int kTablesMaxChunks = 64;
+struct RouteTables {
+    const int32_t *ids;         // [pairs]
+    int32_t *offsets, *counts, *pair_row, *hist;
+    int64_t *row_token;         // [rows]
+    int64_t pairs, rows;
+    int k, E, pad;
+    // set by the launcher
+    int64_t chunk;
+    int chunks, id_bits;
+};
+int64_t route_tables_chunk(int64_t pairs);
+hipError_t launch_route_tables(RouteTables a, hipStream_t stream);
+
+// Expert rows back to tokens (combine.hip)
+struct CombineArgs {
+    const void *y;              // [rows][H]
+    const int32_t *pair_row;    // [T][k]
+    const float *w;             // [T][k]
+    void *out;                  // [T][H]
+    const void *d_out;          // [T][H], backward only
+    const int64_t *row_token;   // [rows], backward only
+    void *d_y;                  // [rows][H], backward only
+    float *d_w;                 // [T][k], backward only
+    int64_t T, rows, H;
+    int k;
+};
+hipError_t launch_combine(const CombineArgs &a, bool bf16, hipStream_t stream);
+hipError_t launch_combine_backward(const CombineArgs &a, bool bf16, hipStream_t stream);
+
+// Token log-probabilities (logprobs.hip)
+constexpr int kLogprobsMaxTop = 64;
+struct LogprobsArgs {
+    const void *x;              // logits [T][ld]
+    int64_t ld, T, V;
+    const int64_t *targets;     // [T]
+    double temperature;
+    int top;
+    float *logprobs, *entropy, *stats;      // [T], [T], [T][2]; read by the backward (entropy, stats)
+    float *top_logprobs;                    // [T][top]
+    int64_t *top_ids;                       // [T][top]
+    void *workspace;
+    const float *d_logprobs, *d_entropy;    // [T], either may be null
+    void *dx;                               // [T][ld_out]
+    int64_t ld_out;
+    // set by the launcher
+    float scale, inv, inv_low;              // log2(e) / temperature; 1 / temperature in two parts
+    int64_t slice;
+    int slices;
+};
+int64_t logprobs_workspace_bytes(int64_t T, int64_t V, int top, int cus);
+hipError_t launch_logprobs(LogprobsArgs a, bool bf16, size_t workspace_bytes, hipStream_t stream);
+hipError_t launch_logprobs_backward(LogprobsArgs a, bool bf16, hipStream_t stream);
+
 // Packed weight layout geometry (see mxfp8_repack in include/mxfp8.h).
 constexpr int64_t kPanelRows = 256;   // rows per packed panel
 constexpr int64_t kKStep = 128;       // K bytes per packed k-step (one MFMA K)

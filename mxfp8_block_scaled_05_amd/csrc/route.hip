@@ -1,0 +1,488 @@
+// Expert routing: the choice of every token's experts and their weights, the
+// gradient of those weights, and the padded, expert-sorted row tables that
+// the gather quantizers and grouped GEMMs read.
+#include "mx_launch.hpp"
+#include "mx_wave.hpp"
+
+namespace mx {
+
+namespace {
+
+constexpr int kBlock = 256;
+
+// NV values of a lane, count of them in the row (the rest become `pad`).
+template <int NV, class E>
+__device__ __forceinline__ void load_values(const E *p, int count, float pad, float (&x)[NV]) {
+    if constexpr (NV >= Elem<E>::kVec) {
+        if (count == NV) {
+#pragma unroll
+            for (int i = 0; i < NV; i += Elem<E>::kVec) Elem<E>::unpack(load16(p + i), x + i);
+            return;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) x[i] = i < count ? Elem<E>::get(p[i]) : pad;
+}
+
+// Reduction over aligned groups of 2^shift lanes, shift known at run time
+// (the same in all lanes).
+template <class T, class Op>
+__device__ __forceinline__ T reduce_shift(T v, int shift, Op op) {
+    if (shift > 0) v = op(v, partner<0>(v));
+    if (shift > 1) v = op(v, partner<1>(v));
+    if (shift > 2) v = op(v, partner<2>(v));
+    if (shift > 3) v = op(v, partner<3>(v));
+    if (shift > 4) v = op(v, partner<4>(v));
+    if (shift > 5) v = op(v, partner<5>(v));
+    return v;
+}
+
+__device__ __forceinline__ uint64_t shfl64(uint64_t v, int lane) {
+    const uint32_t lo = (uint32_t)__shfl((int)(uint32_t)v, lane, 64);
+    const uint32_t hi = (uint32_t)__shfl((int)(uint32_t)(v >> 32), lane, 64);
+    return ((uint64_t)hi << 32) | lo;
+}
+
+template <int W>
+__device__ __forceinline__ uint64_t group_max64(uint64_t v) {
+#pragma unroll
+    for (int d = 1; d < W; d <<= 1) {
+        const uint64_t o = shfl64(v, (int)(threadIdx.x & 63) ^ d);
+        v = o > v ? o : v;
+    }
+    return v;
+}
+
+// Lowest lane of the caller's group of L lanes whose bit is set in `b`,
+// relative to the group (L if none).
+template <int L>
+__device__ __forceinline__ int first_lane(uint64_t b, int seg) {
+    if constexpr (L == 64) {
+        return b ? __builtin_ctzll(b) : L;
+    } else {
+        const uint32_t m = (uint32_t)(b >> seg) & (uint32_t)((1ull << L) - 1);
+        return m ? __builtin_ctz(m) : L;
+    }
+}
+
+// The lanes of one token: group (of experts) g, first expert of the lane and
+// how many it holds.
+struct LaneExperts {
+    int g, first, count;
+};
+template <int NV>
+__device__ __forceinline__ LaneExperts lane_experts(const RouteArgs &a, int l) {
+    const int g = l >> a.lanes_shift, q = l & ((1 << a.lanes_shift) - 1);
+    LaneExperts e;
+    e.g = g;
+    e.first = g * a.size + q * NV;
+    const int left = a.size - q * NV;
+    e.count = g < a.groups ? (left < 0 ? 0 : left > NV ? NV : left) : 0;
+    return e;
+}
+
+// The choice in fp64, for the tokens of a wave of which one has two
+// candidates closer than fp32 can order: the same steps as route_kernel's,
+// on 64-bit keys.  sel[j] of every token gets the j-th expert.
+template <int L, int NV, class E>
+__device__ __noinline__ void choose_fp64(const RouteArgs &a, const E *row, const float *bias, int lane, int *sel) {
+    const int seg = lane & ~(L - 1), l = lane & (L - 1);
+    const LaneExperts ex = lane_experts<NV>(a, l);
+    double c[NV];
+    double top = -__builtin_inf();
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        c[i] = i < ex.count ? (double)Elem<E>::get(row[ex.first + i]) : -__builtin_inf();
+        top = c[i] > top ? c[i] : top;
+    }
+    if (a.sigmoid) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) c[i] = 1.0 / (1.0 + exp(-c[i]));
+    } else {
+#pragma unroll
+        for (int d = 1; d < L; d <<= 1) {
+            const double o = __shfl_xor(top, d, 64);
+            top = o > top ? o : top;
+        }
+        double sum = 0.0;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            c[i] = i < ex.count ? exp(c[i] - top) : 0.0;
+            sum += c[i];
+        }
+#pragma unroll
+        for (int d = 1; d < L; d <<= 1) sum += __shfl_xor(sum, d, 64);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) c[i] = c[i] / sum;
+    }
+    if (bias) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (i < ex.count) c[i] += (double)bias[ex.first + i];
+    }
+    bool keep = ex.g < a.groups;
+    if (a.groups > 1) {
+        double b1 = -__builtin_inf(), b2 = -__builtin_inf();
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            if (i < ex.count) {
+                if (c[i] > b1) {
+                    b2 = b1;
+                    b1 = c[i];
+                } else if (c[i] > b2) {
+                    b2 = c[i];
+                }
+            }
+        }
+        for (int d = 1; d < (1 << a.lanes_shift); d <<= 1) {
+            const double o1 = __shfl_xor(b1, d, 64), o2 = __shfl_xor(b2, d, 64);
+            const double low = o1 < b1 ? o1 : b1, second = o2 > b2 ? o2 : b2;
+            b1 = o1 > b1 ? o1 : b1;
+            b2 = low > second ? low : second;
+        }
+        const uint64_t mine = order_key(a.group_top == 2 ? b1 + b2 : b1);
+        int rank = 0;
+        for (int g = 0; g < a.groups; ++g) {
+            const uint64_t o = shfl64(mine, seg + (g << a.lanes_shift));
+            rank += (o > mine || (o == mine && g < ex.g)) ? 1 : 0;
+        }
+        keep = keep && rank < a.kept;
+    }
+    uint32_t left = keep ? (1u << ex.count) - 1u : 0u;    // experts of the lane still to choose from
+    for (int j = 0; j < a.k; ++j) {
+        uint64_t best = 0;
+        int at = 0;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            uint64_t key = order_key(c[i]);
+            key = key ? key : 1;
+            if (((left >> i) & 1u) && key > best) {
+                best = key;
+                at = i;
+            }
+        }
+        const uint64_t M = group_max64<L>(best);
+        const int own = first_lane<L>(__ballot(best == M), seg);
+        if (l == own) {
+            left &= ~(1u << at);
+            sel[j] = ex.first + at;
+        }
+    }
+}
+
+// Experts and weights of every token.
+//
+// s = softmax(x) or sigmoid(x); c = s (+ bias) chooses: with groups, a
+// group's score is its largest c or the sum of its two largest, and the best
+// `kept` groups stay; ids are the k largest c left, lowest index first among
+// equals; w = s[ids], over their sum if renormalized, times scale.
+//
+// L lanes hold one token, NV neighbouring experts each (64 / L tokens a
+// wave), with the lanes of an expert group next to each other, so group
+// scores and the k choices are reductions over lanes of one row of 16 where
+// they fit (vector-ALU permutes, no LDS).  A choice keeps one number per
+// lane, the largest key not yet taken: 28 bits of the ordered value and the
+// place in the lane.  After a lane gives its head away, the next one is the
+// largest key below it, max((key - head) mod 2^32), which needs no marking of
+// taken experts.
+//
+// fp32 cannot order two scores that differ by less than its rounding, so
+// neighbours in the chosen order (and the last kept and first dropped group)
+// that are closer than 2^-18 of their size send the wave through
+// choose_fp64.  Without a bias the order of s is that of x: bf16 logits are
+// then compared exactly (16 bits of value fit the key).
+template <int L, int NV, class E>
+__global__ __launch_bounds__(kBlock) void route_kernel(const RouteArgs a) {
+    __shared__ int sel[kBlock / L][kRouteMaxK];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int seg = lane & ~(L - 1), l = lane & (L - 1);
+    const int slot = wave * (64 / L) + lane / L;
+    const int64_t token = (int64_t)blockIdx.x * (kBlock / L) + slot;
+    const bool live = token < a.T;
+    const E *row = static_cast<const E *>(a.x) + (live ? token : a.T - 1) * a.ld;
+    const LaneExperts ex = lane_experts<NV>(a, l);
+    const float kNone = -__builtin_inff();
+
+    float v[NV];
+    load_values<NV>(row + (ex.count ? ex.first : 0), ex.count, kNone, v);
+    float top = v[0];
+#pragma unroll
+    for (int i = 1; i < NV; ++i) top = __builtin_fmaxf(top, v[i]);
+    top = group_reduce<L>(top, OpMax());
+
+    float inv = 1.0f, largest = 1.0f;            // 1 / sum of the softmax; largest score at most
+    float s[NV];
+    if (a.sigmoid) {
+        if (!a.order_x) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) s[i] = sigmoid(v[i]);
+        }
+    } else {
+        float sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            s[i] = i < ex.count ? exp_neg(v[i] - top) : 0.0f;
+            sum += s[i];
+        }
+        sum = group_reduce<L>(sum, OpAdd());
+        inv = 1.0f / sum;
+        largest = inv;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) s[i] *= inv;
+    }
+    if (!a.order_x) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) v[i] = s[i];
+        if (a.bias) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                if (i < ex.count) v[i] += a.bias[ex.first + i];
+        }
+    }
+
+    // error of c in fp32: score and sum within 2^-20 of the largest score, the
+    // addition and the key's cut within 2^-19 of c
+    const float kRel = 0x1p-18f;
+    bool close = false;
+    bool keep = ex.g < a.groups;
+    if (a.groups > 1) {
+        float b1 = kNone, b2 = kNone;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const float y = i < ex.count ? v[i] : kNone;
+            b2 = __builtin_fmaxf(b2, __builtin_fminf(b1, y));
+            b1 = __builtin_fmaxf(b1, y);
+        }
+#pragma unroll
+        for (int step = 0; step < 6; ++step) {
+            if (step >= a.lanes_shift) break;
+            float o1, o2;
+            switch (step) {
+                case 0: o1 = partner<0>(b1); o2 = partner<0>(b2); break;
+                case 1: o1 = partner<1>(b1); o2 = partner<1>(b2); break;
+                case 2: o1 = partner<2>(b1); o2 = partner<2>(b2); break;
+                case 3: o1 = partner<3>(b1); o2 = partner<3>(b2); break;
+                case 4: o1 = partner<4>(b1); o2 = partner<4>(b2); break;
+                default: o1 = partner<5>(b1); o2 = partner<5>(b2); break;
+            }
+            b2 = __builtin_fmaxf(__builtin_fminf(b1, o1), __builtin_fmaxf(b2, o2));
+            b1 = __builtin_fmaxf(b1, o1);
+        }
+        const float score = a.group_top == 2 ? b1 + b2 : b1;
+        const uint32_t mine = order_key(score);
+        int rank = 0;
+        for (int g = 0; g < a.groups; ++g) {
+            const uint32_t o = (uint32_t)__shfl((int)mine, seg + (g << a.lanes_shift), 64);
+            rank += (o > mine || (o == mine && g < ex.g)) ? 1 : 0;
+        }
+        const bool in = keep;
+        keep = keep && rank < a.kept;
+        if (!a.order_x) {
+            const float low = group_reduce<L>(keep ? score : __builtin_inff(), OpMin());
+            const float high = group_reduce<L>(in && !keep ? score : kNone, OpMax());
+            close = !(low - high > kRel * (2.0f * largest + __builtin_fabsf(low) + __builtin_fabsf(high)));
+        }
+    }
+
+    uint32_t key[NV];
+    uint32_t head = 0;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        uint32_t u = order_key(v[i]);
+        u = u > 16u ? u : 16u;
+        key[i] = (i < ex.count && keep) ? ((u & ~15u) | (uint32_t)(15 - i)) : 0u;
+        head = key[i] > head ? key[i] : head;
+    }
+    uint32_t mine = 0;                             // lane j: the j-th largest key
+    const int rounds = a.k + (a.order_exact ? 0 : 1);
+    for (int j = 0; j < rounds; ++j) {
+        const uint32_t hv = head & ~15u;
+        const uint32_t M = group_reduce<L>(hv, OpMax());
+        const int own = first_lane<L>(__ballot(hv == M), seg);
+        if (l == j) mine = M;
+        if (l == own) {
+            if (j < a.k) sel[slot][j] = ex.first + 15 - (int)(head & 15u);
+            uint32_t d = 0u - head;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const uint32_t e = key[i] - head;
+                d = e > d ? e : d;
+            }
+            head += d;
+        }
+    }
+    if (!a.order_exact) {
+        const uint32_t next = (uint32_t)__shfl_down((int)mine, 1, 64);
+        if (l < a.k && l + 1 < a.candidates) {
+            const float x0 = order_value(mine), x1 = order_value(next);
+            if (a.order_x) close = close || mine == next;
+            else close = close || !(x0 - x1 > kRel * (largest + __builtin_fabsf(x0)));
+        }
+        if (__ballot(close && live)) {
+            __builtin_amdgcn_wave_barrier();
+            choose_fp64<L, NV, E>(a, row, a.bias, lane, sel[slot]);
+        }
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+
+    int id = 0;
+    float w = 0.0f;
+    if (l < a.k) {
+        id = sel[slot][l];
+        const float x = Elem<E>::get(row[id]);
+        w = a.sigmoid ? sigmoid(x) : exp_neg(x - top) * inv;
+    }
+    if (a.renorm) w = w / group_reduce<L>(w, OpAdd());
+    if (live && l < a.k) {
+        a.ids[token * a.k + l] = id;
+        a.w[token * a.k + l] = w * a.scale;
+    }
+}
+
+// Gradient of the weights with respect to the logits.
+//
+// With g = d_w * scale, a = s[ids], A = sum a: renormalized weights a / A give
+// ds = (g - sum(g a) / A) / A on the chosen experts, else ds = g.  softmax:
+// dx = s (ds - sum(ds a)) over all experts; sigmoid: dx = ds s (1 - s) on the
+// chosen ones, 0 elsewhere.  One read of the logits (softmax) and one write;
+// lanes as in route_kernel, the chosen experts' ds spread over the row
+// through LDS.
+template <int L, int NV, class E>
+__global__ __launch_bounds__(kBlock) void route_backward_kernel(const RouteArgs a) {
+    __shared__ float full[kBlock / L][L * NV];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int l = lane & (L - 1);
+    const int slot = wave * (64 / L) + lane / L;
+    const int64_t token = (int64_t)blockIdx.x * (kBlock / L) + slot;
+    const bool live = token < a.T;
+    const int64_t t = live ? token : a.T - 1;
+    const E *row = static_cast<const E *>(a.x) + t * a.ld;
+    const int first = l * NV;
+    int count = a.E - first;
+    count = count < 0 ? 0 : count > NV ? NV : count;
+
+    float *mine = &full[slot][first];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) mine[i] = 0.0f;
+    int id = -1;
+    float g = 0.0f, x = 0.0f;
+    if (l < a.k) {
+        id = a.ids[t * a.k + l];
+        g = a.dw[t * a.k + l] * a.scale;
+        if (id < 0 || id >= a.E) id = -1;
+        else x = Elem<E>::get(row[id]);
+    }
+    float s[NV], inv = 1.0f, top = 0.0f;
+    if (!a.sigmoid) {
+        float v[NV];
+        load_values<NV>(row + (count ? first : 0), count, -__builtin_inff(), v);
+        top = v[0];
+#pragma unroll
+        for (int i = 1; i < NV; ++i) top = __builtin_fmaxf(top, v[i]);
+        top = group_reduce<L>(top, OpMax());
+        float sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            s[i] = i < count ? exp_neg(v[i] - top) : 0.0f;
+            sum += s[i];
+        }
+        inv = 1.0f / group_reduce<L>(sum, OpAdd());
+    }
+    float chosen = 0.0f;
+    if (id >= 0) chosen = a.sigmoid ? sigmoid(x) : exp_neg(x - top) * inv;
+    else g = 0.0f;
+    float ga = group_reduce<L>(g * chosen, OpAdd());
+    if (a.renorm) {
+        const float A = group_reduce<L>(chosen, OpAdd());
+        g = (g - ga / A) / A;
+        ga = group_reduce<L>(id >= 0 ? g * chosen : 0.0f, OpAdd());
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    if (id >= 0) full[slot][id] = a.sigmoid ? g * chosen * (1.0f - chosen) : g;
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    float d[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) d[i] = a.sigmoid ? mine[i] : s[i] * inv * (mine[i] - ga);
+    if (!live) return;
+    E *out = static_cast<E *>(a.dx) + token * a.E + first;
+    if constexpr (NV >= Elem<E>::kVec) {
+        if (count == NV) {
+#pragma unroll
+            for (int i = 0; i < NV; i += Elem<E>::kVec) store16(out + i, Elem<E>::pack(d + i));
+            return;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+        if (i < count) out[i] = Elem<E>::put(d[i]);
+}
+
+template <int L, int NV>
+void start_route(const RouteArgs &a, bool bf16, bool backward, hipStream_t stream) {
+    const unsigned grid = (unsigned)ceil_div(a.T, kBlock / L);
+    if (backward) {
+        if (bf16) route_backward_kernel<L, NV, uint16_t><<<grid, kBlock, 0, stream>>>(a);
+        else route_backward_kernel<L, NV, float><<<grid, kBlock, 0, stream>>>(a);
+    } else {
+        if (bf16) route_kernel<L, NV, uint16_t><<<grid, kBlock, 0, stream>>>(a);
+        else route_kernel<L, NV, float><<<grid, kBlock, 0, stream>>>(a);
+    }
+}
+
+// Lanes per token L and experts per lane NV: as few lanes as hold the experts
+// at 16 a lane (more tokens a wave, shorter reductions), at least 16 and more
+// than k.
+hipError_t start(RouteArgs a, bool bf16, bool backward, hipStream_t stream) {
+    int groups2 = 1, gshift = 0;
+    while (groups2 < a.groups) groups2 <<= 1, ++gshift;
+    int shift = 4;
+    int64_t nv = 0;
+    for (;; ++shift) {
+        if ((1 << shift) <= a.k || shift < gshift) continue;
+        a.lanes_shift = shift - gshift;
+        nv = ceil_div(a.size, (int64_t)1 << a.lanes_shift);
+        if (nv <= 16) break;
+        if (shift == 6) return hipErrorInvalidValue;
+    }
+    if (shift == 4) {
+        if (nv == 1) start_route<16, 1>(a, bf16, backward, stream);
+        else if (nv == 2) start_route<16, 2>(a, bf16, backward, stream);
+        else if (nv <= 4) start_route<16, 4>(a, bf16, backward, stream);
+        else if (nv <= 8) start_route<16, 8>(a, bf16, backward, stream);
+        else start_route<16, 16>(a, bf16, backward, stream);
+    } else if (shift == 5) {
+        if (nv <= 8) start_route<32, 8>(a, bf16, backward, stream);
+        else start_route<32, 16>(a, bf16, backward, stream);
+    } else {
+        if (nv <= 8) start_route<64, 8>(a, bf16, backward, stream);
+        else start_route<64, 16>(a, bf16, backward, stream);
+    }
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_route(const RouteArgs &args, bool bf16, hipStream_t stream) {
+    RouteArgs a = args;
+    if (a.kept == a.groups) {                        // every group stays: one group
+        a.groups = a.kept = 1;
+        a.size = a.E;
+    }
+    // without a bias s rises with x, so the choice (and a group's largest) can be read off x
+    a.order_x = !a.bias && (a.groups == 1 || a.group_top == 1);
+    a.order_exact = a.order_x && bf16;
+    a.candidates = a.kept * a.size;
+    return start(a, bf16, false, stream);
+}
+
+hipError_t launch_route_backward(const RouteArgs &args, bool bf16, hipStream_t stream) {
+    RouteArgs a = args;
+    a.groups = a.kept = 1;
+    a.size = a.E;
+    return start(a, bf16, true, stream);
+}
+
+}  // namespace mx

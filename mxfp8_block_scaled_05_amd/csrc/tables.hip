@@ -1,0 +1,159 @@
+// The expert-sorted row tables of a routed batch.
+#include "mx_launch.hpp"
+#include "mx_wave.hpp"
+
+namespace mx {
+
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kWavesT = kThreads / 64;
+
+__device__ __forceinline__ bool real_expert(int id, int E) { return (unsigned)id < (unsigned)E; }
+
+// counts of the experts in one chunk of pairs -> hist[chunk][E]
+__global__ __launch_bounds__(kThreads) void route_count_kernel(const RouteTables a) {
+    __shared__ int cnt[kTablesMaxExperts];
+    for (int e = threadIdx.x; e < a.E; e += kThreads) cnt[e] = 0;
+    __syncthreads();
+    const int64_t lo = (int64_t)blockIdx.x * a.chunk;
+    const int64_t hi = lo + a.chunk < a.pairs ? lo + a.chunk : a.pairs;
+    for (int64_t p = lo + threadIdx.x; p < hi; p += kThreads) {
+        const int id = a.ids[p];
+        if (real_expert(id, a.E)) atomicAdd(&cnt[id], 1);
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < a.E; e += kThreads) a.hist[(int64_t)blockIdx.x * a.E + e] = cnt[e];
+}
+
+// Places a chunk's pairs: row = start of the expert's padded group + pairs of
+// that expert in earlier chunks, earlier waves of the chunk, and earlier in
+// the wave, so rows come in (expert, pair) order whatever runs first.  The
+// rank inside a wave is the count of lower lanes with the same expert, found
+// with one ballot per bit of the id.  One chunk needs no counts from before.
+__global__ __launch_bounds__(kThreads) void route_place_kernel(const RouteTables a) {
+    __shared__ int start[kTablesMaxExperts + 1];     // padded group starts
+    __shared__ int total[kTablesMaxExperts];
+    __shared__ int at[kWavesT][kTablesMaxExperts];   // next row of (wave, expert)
+    __shared__ int sums[kWavesT];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    for (int i = tid; i < kWavesT * kTablesMaxExperts; i += kThreads) (&at[0][0])[i] = 0;
+    __syncthreads();
+
+    const int64_t lo = (int64_t)blockIdx.x * a.chunk;
+    const int64_t hi = lo + a.chunk < a.pairs ? lo + a.chunk : a.pairs;
+    const int64_t per = a.chunk / kWavesT;           // pairs of a wave, a multiple of 64
+    const int64_t wlo = lo + wave * per;
+    const int64_t whi = wlo + per < hi ? wlo + per : hi;
+    for (int64_t p = wlo + lane; p < whi; p += 64) {
+        const int id = a.ids[p];
+        if (real_expert(id, a.E)) atomicAdd(&at[wave][id], 1);
+    }
+    __syncthreads();
+
+    // totals over all chunks, pairs before this chunk
+    constexpr int kPer = kTablesMaxExperts / kThreads;
+    int before[kPer], padded[kPer];
+    int mine = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const int e = tid * kPer + i;
+        int all = 0, pre = 0;
+        if (e < a.E) {
+            if (a.chunks == 1) {
+                for (int w = 0; w < kWavesT; ++w) all += at[w][e];
+            } else {
+                for (int c = 0; c < a.chunks; ++c) {
+                    const int n = a.hist[(int64_t)c * a.E + e];
+                    pre += c < (int)blockIdx.x ? n : 0;
+                    all += n;
+                }
+            }
+            total[e] = all;
+        }
+        before[i] = pre;
+        padded[i] = (all + a.pad - 1) / a.pad * a.pad;
+        mine += padded[i];
+    }
+    // exclusive scan of the padded totals over the experts
+    int scan = mine;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int o = __shfl_up(scan, d, 64);
+        scan += lane >= d ? o : 0;
+    }
+    if (lane == 63) sums[wave] = scan;
+    __syncthreads();
+    int run = scan - mine;
+    for (int w = 0; w < wave; ++w) run += sums[w];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const int e = tid * kPer + i;
+        if (e < a.E) {
+            start[e] = run;
+            int next = run + before[i];
+            for (int w = 0; w < kWavesT; ++w) {
+                const int n = at[w][e];
+                at[w][e] = next;
+                next += n;
+            }
+            if (e == a.E - 1) start[a.E] = run + padded[i];
+        }
+        run += padded[i];
+    }
+    __syncthreads();
+
+    for (int64_t base = wlo; base < whi; base += 64) {
+        const int64_t p = base + lane;
+        const int id = p < whi ? a.ids[p] : -1;
+        const bool real = real_expert(id, a.E);
+        uint64_t same = __ballot(real);
+        for (int b = 0; b < a.id_bits; ++b) {
+            const uint64_t m = __ballot((id >> b) & 1);
+            same &= ((id >> b) & 1) ? m : ~m;
+        }
+        const uint64_t lower = same & ((1ull << lane) - 1);
+        const int rank = __builtin_popcountll(lower);
+        int row = -1;
+        if (real) row = at[wave][id] + rank;
+        __builtin_amdgcn_wave_barrier();
+        if (real && (same >> lane) == 1ull) at[wave][id] = row + 1;   // highest lane of its expert
+        __builtin_amdgcn_wave_barrier();
+        if (p < whi) {
+            a.pair_row[p] = row;
+            if (real) a.row_token[row] = p / a.k;
+        }
+    }
+
+    // padding rows, the rows past the last group, and the tables of the groups
+    for (int e = blockIdx.x * kWavesT + wave; e < a.E; e += gridDim.x * kWavesT)
+        for (int r = start[e] + total[e] + lane; r < start[e + 1]; r += 64) a.row_token[r] = -1;
+    for (int64_t r = start[a.E] + (int64_t)blockIdx.x * kThreads + tid; r < a.rows; r += (int64_t)gridDim.x * kThreads)
+        a.row_token[r] = -1;
+    if (blockIdx.x == 0) {
+        for (int e = tid; e <= a.E; e += kThreads) a.offsets[e] = start[e];
+        for (int e = tid; e < a.E; e += kThreads) a.counts[e] = total[e];
+    }
+}
+
+}  // namespace
+
+// Chunks of pairs, one block each: one chunk while a block can place them in
+// a few steps, then at most kTablesMaxChunks.
+int64_t route_tables_chunk(int64_t pairs) {
+    int64_t chunk = 2 * kThreads;
+    if (ceil_div(pairs, chunk) > kTablesMaxChunks) chunk = ceil_div(ceil_div(pairs, kTablesMaxChunks), kThreads) * kThreads;
+    return chunk;
+}
+
+hipError_t launch_route_tables(RouteTables a, hipStream_t stream) {
+    a.chunk = route_tables_chunk(a.pairs);
+    a.chunks = (int)ceil_div(a.pairs, a.chunk);
+    a.id_bits = 0;
+    while ((1 << a.id_bits) < a.E) ++a.id_bits;
+    if (a.chunks > 1) route_count_kernel<<<(unsigned)a.chunks, kThreads, 0, stream>>>(a);
+    route_place_kernel<<<(unsigned)a.chunks, kThreads, 0, stream>>>(a);
+    return hipGetLastError();
+}
+
+}  // namespace mx

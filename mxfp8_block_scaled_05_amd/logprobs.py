@@ -1,0 +1,94 @@
+"""Token log-probabilities, entropy and top alternatives of logits, and their
+gradient (include/mxfp8_tokens.h).
+
+    r = token_logprobs(logits, targets, temperature=1.0, top_n=0)
+    d = token_logprobs_backward(logits, targets, r.stats, r.entropy, d_logprobs, d_entropy)
+"""
+from __future__ import annotations
+
+from dataclasses import dataclass
+
+import torch
+
+from . import _check, _need, _ptr, _stream
+from ._tokens import need_rows, same_device, tokens_lib
+
+
+@dataclass
+class TokenLogprobs:
+    logprobs: torch.Tensor                  # fp32 [T]: log p of the targets, 0 where there is none
+    entropy: torch.Tensor                   # fp32 [T]
+    stats: torch.Tensor                     # fp32 [T, 2]: max and log sum of exp(z - max), for the gradient
+    top_logprobs: torch.Tensor | None       # fp32 [T, top_n]
+    top_ids: torch.Tensor | None            # int64 [T, top_n]
+
+
+def _logits_targets(logits, targets):
+    code, ld = need_rows(logits, "logits")
+    _need(targets, torch.int64, "targets")
+    T, V = logits.shape
+    if targets.numel() != T:
+        raise ValueError("targets must have T = %d entries" % T)
+    same_device(logits, targets)
+    return code, ld, T, V
+
+
+def token_logprobs(logits: torch.Tensor, targets: torch.Tensor, *, temperature: float = 1.0,
+                   top_n: int = 0) -> TokenLogprobs:
+    """Log-probability of ``targets`` (int64 [T]; outside [0, V): none, 0) under
+    softmax(logits / temperature), the entropy, and the ``top_n`` (at most 64)
+    likeliest columns with theirs, from one pass over logits (fp32 or bf16
+    [T, V], rows contiguous, any row stride) (mxfp8_token_logprobs)."""
+    code, ld, T, V = _logits_targets(logits, targets)
+    L = tokens_lib()
+    dev = logits.device
+    logprobs = torch.empty(T, dtype=torch.float32, device=dev)
+    entropy = torch.empty(T, dtype=torch.float32, device=dev)
+    stats = torch.empty((T, 2), dtype=torch.float32, device=dev)
+    top = ids = None
+    if top_n:
+        top = torch.empty((T, top_n), dtype=torch.float32, device=dev)
+        ids = torch.empty((T, top_n), dtype=torch.int64, device=dev)
+    need = int(L.mxfp8_token_logprobs_workspace_bytes(T, V, top_n))
+    ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    _check(L.mxfp8_token_logprobs(_ptr(logits), code, ld, T, V, _ptr(targets), temperature, top_n, _ptr(logprobs),
+                                  _ptr(entropy), _ptr(stats), _ptr(top) if top_n else None,
+                                  _ptr(ids) if top_n else None, _ptr(ws) if need else None, need, _stream(dev)),
+           "mxfp8_token_logprobs")
+    return TokenLogprobs(logprobs, entropy, stats, top, ids)
+
+
+def token_logprobs_backward(logits: torch.Tensor, targets: torch.Tensor, stats: torch.Tensor,
+                            entropy: torch.Tensor | None, d_logprobs: torch.Tensor | None,
+                            d_entropy: torch.Tensor | None = None, *, temperature: float = 1.0,
+                            out: torch.Tensor | None = None) -> torch.Tensor:
+    """Gradient of token_logprobs' logprobs and entropy with respect to the
+    logits, in their dtype (mxfp8_token_logprobs_backward).  Either gradient
+    may be None.  ``out`` may be the logits themselves (in place)."""
+    code, ld, T, V = _logits_targets(logits, targets)
+    if d_logprobs is None and d_entropy is None:
+        raise ValueError("give d_logprobs, d_entropy or both")
+    if d_entropy is not None and entropy is None:
+        raise ValueError("d_entropy needs entropy")
+    _need(stats, torch.float32, "stats")
+    if tuple(stats.shape) != (T, 2):
+        raise ValueError("stats must be [T, 2]")
+    for t, name in ((entropy, "entropy"), (d_logprobs, "d_logprobs"), (d_entropy, "d_entropy")):
+        if t is not None:
+            _need(t, torch.float32, name)
+            if t.numel() != T:
+                raise ValueError("%s must have T = %d entries" % (name, T))
+    same_device(logits, stats, entropy, d_logprobs, d_entropy)
+    if out is None:
+        out = torch.empty((T, V), dtype=logits.dtype, device=logits.device)
+        ld_out = V
+    else:
+        out_code, ld_out = need_rows(out, "out")
+        if out_code != code or tuple(out.shape) != (T, V):
+            raise ValueError("out must be [T, V] in the logits' dtype")
+        same_device(logits, out)
+    _check(tokens_lib().mxfp8_token_logprobs_backward(
+        _ptr(logits), code, ld, T, V, _ptr(targets), _ptr(stats), _ptr(entropy) if entropy is not None else None,
+        _ptr(d_logprobs) if d_logprobs is not None else None, _ptr(d_entropy) if d_entropy is not None else None,
+        temperature, _ptr(out), ld_out, _stream(logits.device)), "mxfp8_token_logprobs_backward")
+    return out
