@@ -201,7 +201,7 @@ struct RouteTables {
     int k, E, pad;
     // set by the launcher
     int64_t chunk;
-    int chunks, id_bits;
+    int chunks, id_bits, width;
 };
 int64_t route_tables_chunk(int64_t pairs);
 hipError_t launch_route_tables(RouteTables a, hipStream_t stream);

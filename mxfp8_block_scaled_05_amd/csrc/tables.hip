@@ -36,8 +36,11 @@ __global__ __launch_bounds__(kThreads) void route_place_kernel(const RouteTables
     __shared__ int total[kTablesMaxExperts];
     __shared__ int at[kWavesT][kTablesMaxExperts];   // next row of (wave, expert)
     __shared__ int sums[kWavesT];
+    __shared__ int2 joined[kThreads];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    for (int i = tid; i < kWavesT * kTablesMaxExperts; i += kThreads) (&at[0][0])[i] = 0;
+    for (int e = tid; e < a.E; e += kThreads)
+#pragma unroll
+        for (int w = 0; w < kWavesT; ++w) at[w][e] = 0;
     __syncthreads();
 
     const int64_t lo = (int64_t)blockIdx.x * a.chunk;
@@ -51,57 +54,58 @@ __global__ __launch_bounds__(kThreads) void route_place_kernel(const RouteTables
     }
     __syncthreads();
 
-    // totals over all chunks, pairs before this chunk
-    constexpr int kPer = kTablesMaxExperts / kThreads;
-    int before[kPer], padded[kPer];
-    int mine = 0;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        const int e = tid * kPer + i;
-        int all = 0, pre = 0;
+    // pairs of every expert in all chunks and in the chunks before this one:
+    // `parts` threads an expert, each with every parts-th chunk
+    for (int e0 = 0; e0 < a.E; e0 += kThreads) {
+        const int e = e0 + (tid & (a.width - 1)), part = tid / a.width;
+        int all = 0, before = 0;
         if (e < a.E) {
             if (a.chunks == 1) {
-                for (int w = 0; w < kWavesT; ++w) all += at[w][e];
+                for (int w = part; w < kWavesT; w += kThreads / a.width) all += at[w][e];
             } else {
-                for (int c = 0; c < a.chunks; ++c) {
+#pragma unroll 8
+                for (int c = part; c < a.chunks; c += kThreads / a.width) {
                     const int n = a.hist[(int64_t)c * a.E + e];
-                    pre += c < (int)blockIdx.x ? n : 0;
+                    before += c < (int)blockIdx.x ? n : 0;
                     all += n;
                 }
             }
+        }
+        joined[tid] = make_int2(all, before);
+        __syncthreads();
+        all = before = 0;
+        if (tid < a.width && e < a.E) {
+            for (int q = tid; q < kThreads; q += a.width) {
+                all += joined[q].x;
+                before += joined[q].y;
+            }
             total[e] = all;
         }
-        before[i] = pre;
-        padded[i] = (all + a.pad - 1) / a.pad * a.pad;
-        mine += padded[i];
-    }
-    // exclusive scan of the padded totals over the experts
-    int scan = mine;
+        // exclusive scan of the padded totals over the experts
+        const int padded = (all + a.pad - 1) / a.pad * a.pad;
+        int scan = padded;
 #pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const int o = __shfl_up(scan, d, 64);
-        scan += lane >= d ? o : 0;
-    }
-    if (lane == 63) sums[wave] = scan;
-    __syncthreads();
-    int run = scan - mine;
-    for (int w = 0; w < wave; ++w) run += sums[w];
+        for (int d = 1; d < 64; d <<= 1) {
+            const int o = __shfl_up(scan, d, 64);
+            scan += lane >= d ? o : 0;
+        }
+        if (lane == 63) sums[wave] = scan;
+        __syncthreads();
+        int first = scan - padded + (e0 ? start[e0] : 0);
+        for (int w = 0; w < wave; ++w) first += sums[w];
+        if (tid < a.width && e < a.E) {
+            start[e] = first;
+            start[e + 1] = first + padded;       // the next expert's own start, and the end after the last
+            int next = first + before;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        const int e = tid * kPer + i;
-        if (e < a.E) {
-            start[e] = run;
-            int next = run + before[i];
             for (int w = 0; w < kWavesT; ++w) {
                 const int n = at[w][e];
                 at[w][e] = next;
                 next += n;
             }
-            if (e == a.E - 1) start[a.E] = run + padded[i];
         }
-        run += padded[i];
+        __syncthreads();
     }
-    __syncthreads();
 
     for (int64_t base = wlo; base < whi; base += 64) {
         const int64_t p = base + lane;
@@ -121,7 +125,7 @@ __global__ __launch_bounds__(kThreads) void route_place_kernel(const RouteTables
         __builtin_amdgcn_wave_barrier();
         if (p < whi) {
             a.pair_row[p] = row;
-            if (real) a.row_token[row] = p / a.k;
+            if (real) a.row_token[row] = (uint32_t)p / (uint32_t)a.k;
         }
     }
 
@@ -151,6 +155,8 @@ hipError_t launch_route_tables(RouteTables a, hipStream_t stream) {
     a.chunks = (int)ceil_div(a.pairs, a.chunk);
     a.id_bits = 0;
     while ((1 << a.id_bits) < a.E) ++a.id_bits;
+    a.width = 64;
+    while (a.width < a.E && a.width < kThreads) a.width <<= 1;
     if (a.chunks > 1) route_count_kernel<<<(unsigned)a.chunks, kThreads, 0, stream>>>(a);
     route_place_kernel<<<(unsigned)a.chunks, kThreads, 0, stream>>>(a);
     return hipGetLastError();
