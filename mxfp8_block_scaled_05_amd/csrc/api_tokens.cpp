@@ -112,9 +112,9 @@ mxfp8_status mxfp8_route_tables(const int32_t *ids, int64_t T, int64_t k, int64_
 static mxfp8_status combine_sizes(int64_t rows, int64_t H, int64_t T, int64_t k) {
     if (rows < 0 || rows >= kMaxInt || H < 1 || H >= kMaxInt || T < 0 || T >= kMaxInt || k < 1 || !product_ok(T, k))
         return MXFP8_ERR_SHAPE;
-    // a thread per 4 elements of an output row, a wave per pair
+    // a thread per 4 elements of an output row; a wave per pair and per 8 rows
     if (!product_ok(T, ceil_div(H, 4)) || !grid_ok(ceil_div(T * ceil_div(H, 4), 256)) ||
-        !grid_ok(ceil_div(T * k, 4) + ceil_div(rows, 256)))
+        !grid_ok(ceil_div(T * k, 4) + ceil_div(rows, 32)))
         return MXFP8_ERR_SHAPE;
     return MXFP8_OK;
 }

@@ -8,17 +8,18 @@ namespace mx {
 namespace {
 
 constexpr int kBlock = 256;
+constexpr int kAhead = 8;          // rows of a token in flight
+constexpr int kZeroRows = 8;       // rows a wave looks over for padding
 
-// One 16-byte piece of a row: all of it, or its first n elements.
+// One 16-byte piece of a row: all of it, or its first n elements and zeros.
 template <class E>
-__device__ __forceinline__ void load_piece(const E *p, int n, float *f) {
+__device__ __forceinline__ v4u load_piece(const E *p, int n) {
     constexpr int kV = Elem<E>::kVec;
-    if (n >= kV) {
-        Elem<E>::unpack(load16(p), f);
-    } else {
+    if (n >= kV) return load16(p);
+    float f[kV];
 #pragma unroll
-        for (int i = 0; i < kV; ++i) f[i] = i < n ? Elem<E>::get(p[i]) : 0.0f;
-    }
+    for (int i = 0; i < kV; ++i) f[i] = i < n ? Elem<E>::get(p[i]) : 0.0f;
+    return Elem<E>::pack(f);                             // exact: the values are the type's own
 }
 template <class E>
 __device__ __forceinline__ void store_piece(E *p, int n, const float *f) {
@@ -47,14 +48,26 @@ __global__ __launch_bounds__(kBlock) void combine_kernel(const CombineArgs a, in
     float acc[kV];
 #pragma unroll
     for (int e = 0; e < kV; ++e) acc[e] = 0.0f;
-    for (int j = 0; j < a.k; ++j) {
-        const int row = a.pair_row[t * a.k + j];
-        const float w = a.w[t * a.k + j];
-        if (row < 0 || row >= a.rows) continue;
-        float f[kV];
-        load_piece(y + row * a.H, n, f);
+    for (int j0 = 0; j0 < a.k; j0 += kAhead) {
+        int row[kAhead];
+        float w[kAhead];
+        v4u r[kAhead];
 #pragma unroll
-        for (int e = 0; e < kV; ++e) acc[e] = __builtin_fmaf(w, f[e], acc[e]);
+        for (int u = 0; u < kAhead; ++u) {
+            row[u] = j0 + u < a.k ? a.pair_row[t * a.k + j0 + u] : -1;
+            w[u] = j0 + u < a.k ? a.w[t * a.k + j0 + u] : 0.0f;
+        }
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u)
+            if (row[u] >= 0 && row[u] < a.rows) r[u] = load_piece(y + row[u] * a.H, n);
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u)
+            if (row[u] >= 0 && row[u] < a.rows) {
+                float f[kV];
+                Elem<E>::unpack(r[u], f);
+#pragma unroll
+                for (int e = 0; e < kV; ++e) acc[e] = __builtin_fmaf(w[u], f[e], acc[e]);
+            }
     }
     store_piece(static_cast<E *>(a.out) + t * a.H + col, n, acc);
 }
@@ -78,11 +91,32 @@ __global__ __launch_bounds__(kBlock) void combine_backward_kernel(const CombineA
         if (real) {
             const E *d = static_cast<const E *>(a.d_out) + t * a.H;
             const E *y = static_cast<const E *>(a.y) + row * a.H;
-            for (int64_t col = lane * kV; col < a.H; col += 64 * kV) {
+            int64_t col = lane * kV;
+            for (; col + 3 * 64 * kV + kV <= a.H; col += 4 * 64 * kV) {
+                v4u rg[4], rf[4];
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    rf[u] = load16(y + col + u * 64 * kV);
+                    rg[u] = load16(d + col + u * 64 * kV);
+                }
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    float g[kV], f[kV];
+                    Elem<E>::unpack(rg[u], g);
+                    Elem<E>::unpack(rf[u], f);
+#pragma unroll
+                    for (int e = 0; e < kV; ++e) {
+                        dot = __builtin_fmaf(g[e], f[e], dot);
+                        g[e] *= w;
+                    }
+                    store16(d_y + row * a.H + col + u * 64 * kV, Elem<E>::pack(g));
+                }
+            }
+            for (; col < a.H; col += 64 * kV) {
                 const int n = (int)(a.H - col < kV ? a.H - col : kV);
                 float g[kV], f[kV];
-                load_piece(d + col, n, g);
-                load_piece(y + col, n, f);
+                Elem<E>::unpack(load_piece(d + col, n), g);
+                Elem<E>::unpack(load_piece(y + col, n), f);
 #pragma unroll
                 for (int e = 0; e < kV; ++e) {
                     dot = __builtin_fmaf(g[e], f[e], dot);
@@ -95,11 +129,10 @@ __global__ __launch_bounds__(kBlock) void combine_backward_kernel(const CombineA
         if (lane == 0) a.d_w[p] = dot;
         return;
     }
-    const int64_t base = (((int64_t)blockIdx.x - pair_blocks) * (kBlock / 64) + wave) * 64;
-    if (base >= a.rows) return;
+    const int64_t base = (((int64_t)blockIdx.x - pair_blocks) * (kBlock / 64) + wave) * kZeroRows;
     const int64_t mine = base + lane;
     bool empty = false;
-    if (mine < a.rows) {
+    if (lane < kZeroRows && mine < a.rows) {
         const int64_t t = a.row_token[mine];
         empty = t < 0 || t >= a.T;
     }
@@ -125,7 +158,7 @@ hipError_t launch_combine(const CombineArgs &a, bool bf16, hipStream_t stream) {
 
 hipError_t launch_combine_backward(const CombineArgs &a, bool bf16, hipStream_t stream) {
     const int64_t pair_blocks = ceil_div(a.T * a.k, kBlock / 64);
-    const unsigned grid = (unsigned)(pair_blocks + ceil_div(a.rows, kBlock));
+    const unsigned grid = (unsigned)(pair_blocks + ceil_div(a.rows, kBlock / 64 * kZeroRows));
     if (bf16) combine_backward_kernel<uint16_t><<<grid, kBlock, 0, stream>>>(a, pair_blocks);
     else combine_backward_kernel<float><<<grid, kBlock, 0, stream>>>(a, pair_blocks);
     return hipGetLastError();
