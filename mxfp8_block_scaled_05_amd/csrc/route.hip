@@ -65,6 +65,17 @@ __device__ __forceinline__ int first_lane(uint64_t b, int seg) {
     }
 }
 
+// LDS written by a lane, read by another of its wave
+__device__ __forceinline__ void wave_sync() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
+// 1 / (1 + e^-x) for the choice: 2^x and 1/x of the hardware
+__device__ __forceinline__ float fast_sigmoid(float x) {
+    return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(x * -kLog2E));
+}
+
 // The lanes of one token: group (of experts) g, first expert of the lane and
 // how many it holds.
 struct LaneExperts {
@@ -85,7 +96,7 @@ __device__ __forceinline__ LaneExperts lane_experts(const RouteArgs &a, int l) {
 // candidates closer than fp32 can order: the same steps as route_kernel's,
 // on 64-bit keys.  sel[j] of every token gets the j-th expert.
 template <int L, int NV, class E>
-__device__ __noinline__ void choose_fp64(const RouteArgs &a, const E *row, const float *bias, int lane, int *sel) {
+__device__ __forceinline__ void choose_fp64(const RouteArgs &a, const E *row, const float *bias, int lane, int *sel) {
     const int seg = lane & ~(L - 1), l = lane & (L - 1);
     const LaneExperts ex = lane_experts<NV>(a, l);
     double c[NV];
@@ -188,12 +199,14 @@ __device__ __noinline__ void choose_fp64(const RouteArgs &a, const E *row, const
 //
 // fp32 cannot order two scores that differ by less than its rounding, so
 // neighbours in the chosen order (and the last kept and first dropped group)
-// that are closer than 2^-18 of their size send the wave through
-// choose_fp64.  Without a bias the order of s is that of x: bf16 logits are
+// whose keys are equal, or whose scores are closer than twice their error,
+// send the wave through choose_fp64.  That error is at most 4 half steps of
+// fp32 for a sigmoid, 32 of the largest score for a softmax (half of it the
+// sum's), and one for the bias; `margin` and kRel hold the doubles.  Without a bias the order of s is that of x: bf16 logits are
 // then compared exactly (16 bits of value fit the key).
 template <int L, int NV, class E>
-__global__ __launch_bounds__(kBlock) void route_kernel(const RouteArgs a) {
-    __shared__ int sel[kBlock / L][kRouteMaxK];
+__global__ __launch_bounds__(kBlock, 4) void route_kernel(const RouteArgs a) {
+    __shared__ int sel[kBlock / L][kRouteMaxK + 1];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int seg = lane & ~(L - 1), l = lane & (L - 1);
     const int slot = wave * (64 / L) + lane / L;
@@ -210,39 +223,35 @@ __global__ __launch_bounds__(kBlock) void route_kernel(const RouteArgs a) {
     for (int i = 1; i < NV; ++i) top = __builtin_fmaxf(top, v[i]);
     top = group_reduce<L>(top, OpMax());
 
-    float inv = 1.0f, largest = 1.0f;            // 1 / sum of the softmax; largest score at most
-    float s[NV];
+    // scores for the choice; the weights are computed again from the chosen
+    // logits, at full accuracy
+    float inv = 1.0f, margin = 0x1p-20f;
     if (a.sigmoid) {
         if (!a.order_x) {
 #pragma unroll
-            for (int i = 0; i < NV; ++i) s[i] = sigmoid(v[i]);
+            for (int i = 0; i < NV; ++i) v[i] = fast_sigmoid(v[i]);
         }
     } else {
-        float sum = 0.0f;
+        float s[NV], sum = 0.0f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            s[i] = i < ex.count ? exp_neg(v[i] - top) : 0.0f;
-            sum += s[i];
+            s[i] = __builtin_amdgcn_exp2f((v[i] - top) * kLog2E);
+            sum += i < ex.count ? s[i] : 0.0f;
         }
-        sum = group_reduce<L>(sum, OpAdd());
-        inv = 1.0f / sum;
-        largest = inv;
+        inv = 1.0f / group_reduce<L>(sum, OpAdd());
+        margin = 0x1p-18f * inv;
+        if (!a.order_x) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i) s[i] *= inv;
+            for (int i = 0; i < NV; ++i) v[i] = s[i] * inv;
+        }
     }
-    if (!a.order_x) {
+    if (a.bias) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i) v[i] = s[i];
-        if (a.bias) {
-#pragma unroll
-            for (int i = 0; i < NV; ++i)
-                if (i < ex.count) v[i] += a.bias[ex.first + i];
-        }
+        for (int i = 0; i < NV; ++i)
+            if (i < ex.count) v[i] += a.bias[ex.first + i];
     }
 
-    // error of c in fp32: score and sum within 2^-20 of the largest score, the
-    // addition and the key's cut within 2^-19 of c
-    const float kRel = 0x1p-18f;
+    const float kRel = 0x1p-20f;
     bool close = false;
     bool keep = ex.g < a.groups;
     if (a.groups > 1) {
@@ -280,7 +289,7 @@ __global__ __launch_bounds__(kBlock) void route_kernel(const RouteArgs a) {
         if (!a.order_x) {
             const float low = group_reduce<L>(keep ? score : __builtin_inff(), OpMin());
             const float high = group_reduce<L>(in && !keep ? score : kNone, OpMax());
-            close = !(low - high > kRel * (2.0f * largest + __builtin_fabsf(low) + __builtin_fabsf(high)));
+            close = !(low - high > 2.0f * margin + kRel * (__builtin_fabsf(low) + __builtin_fabsf(high)));
         }
     }
 
@@ -301,7 +310,7 @@ __global__ __launch_bounds__(kBlock) void route_kernel(const RouteArgs a) {
         const int own = first_lane<L>(__ballot(hv == M), seg);
         if (l == j) mine = M;
         if (l == own) {
-            if (j < a.k) sel[slot][j] = ex.first + 15 - (int)(head & 15u);
+            sel[slot][j] = ex.first + 15 - (int)(head & 15u);
             uint32_t d = 0u - head;
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
@@ -311,28 +320,32 @@ __global__ __launch_bounds__(kBlock) void route_kernel(const RouteArgs a) {
             head += d;
         }
     }
+    wave_sync();
+    const int count = rounds < a.candidates ? rounds : a.candidates;       // entries of sel that are experts
+    int id = l < count ? sel[slot][l] : 0;
+    float x = Elem<E>::get(row[id]);
     if (!a.order_exact) {
+        float c = x;
+        if (!a.order_x) {
+            c = a.sigmoid ? fast_sigmoid(x) : __builtin_amdgcn_exp2f((x - top) * kLog2E) * inv;
+            if (a.bias) c += a.bias[id];
+        }
         const uint32_t next = (uint32_t)__shfl_down((int)mine, 1, 64);
-        if (l < a.k && l + 1 < a.candidates) {
-            const float x0 = order_value(mine), x1 = order_value(next);
-            if (a.order_x) close = close || mine == next;
-            else close = close || !(x0 - x1 > kRel * (largest + __builtin_fabsf(x0)));
+        const float below = __shfl_down(c, 1, 64);
+        if (l + 1 < count) {
+            close = close || mine == next;
+            if (!a.order_x) close = close || !(c - below > margin + kRel * __builtin_fabsf(c));
         }
         if (__ballot(close && live)) {
-            __builtin_amdgcn_wave_barrier();
             choose_fp64<L, NV, E>(a, row, a.bias, lane, sel[slot]);
+            wave_sync();
+            id = l < a.k ? sel[slot][l] : 0;
+            x = Elem<E>::get(row[id]);
         }
     }
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
 
-    int id = 0;
     float w = 0.0f;
-    if (l < a.k) {
-        id = sel[slot][l];
-        const float x = Elem<E>::get(row[id]);
-        w = a.sigmoid ? sigmoid(x) : exp_neg(x - top) * inv;
-    }
+    if (l < a.k) w = a.sigmoid ? sigmoid(x) : exp_neg(x - top) * inv;
     if (a.renorm) w = w / group_reduce<L>(w, OpAdd());
     if (live && l < a.k) {
         a.ids[token * a.k + l] = id;
@@ -398,11 +411,9 @@ __global__ __launch_bounds__(kBlock) void route_backward_kernel(const RouteArgs 
         g = (g - ga / A) / A;
         ga = group_reduce<L>(id >= 0 ? g * chosen : 0.0f, OpAdd());
     }
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
+    wave_sync();
     if (id >= 0) full[slot][id] = a.sigmoid ? g * chosen * (1.0f - chosen) : g;
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
+    wave_sync();
     float d[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) d[i] = a.sigmoid ? mine[i] : s[i] * inv * (mine[i] - ga);
