@@ -148,7 +148,9 @@ def _ptr(t: torch.Tensor):
 
 
 def _stream(device: torch.device):
-    return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+    # the handle of torch.cuda.current_stream(device) without the Stream object around it (0.1 us against 2)
+    index = device.index
+    return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if index is None else index))
 
 
 def _need(t: torch.Tensor, dtype, name: str):

@@ -62,6 +62,7 @@ def need_rows(t: torch.Tensor, name: str):
 
 
 def same_device(first: torch.Tensor, *others):
+    d = first.get_device()
     for t in others:
-        if t is not None and t.device != first.device:
+        if t is not None and t.get_device() != d:
             raise ValueError("all tensors must be on one device, got %s and %s" % (first.device, t.device))

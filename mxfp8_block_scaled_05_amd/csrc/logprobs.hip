@@ -7,8 +7,8 @@ namespace mx {
 
 namespace {
 
-constexpr int kBlock = 256;
-constexpr int kWaves = kBlock / 64;
+constexpr int kBlock = 256;         // threads of the gradient's and of split rows' blocks
+constexpr int kWide = 1024;         // threads of a block that has a long row to itself
 constexpr int kUnroll = 4;          // 16-byte loads of a thread in flight
 constexpr float kLowest = -3.402823466e38f;
 
@@ -30,16 +30,17 @@ __device__ __forceinline__ Stats join(const Stats &a, const Stats &b, float c) {
     return r;
 }
 
+template <int STEP>
+__device__ __forceinline__ Stats join_step(const Stats &v, float c) {
+    return join(v, Stats{partner<STEP>(v.m), partner<STEP>(v.s), partner<STEP>(v.w)}, c);
+}
 __device__ __forceinline__ Stats join_lanes(Stats v, float c) {
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        Stats o;
-        o.m = __shfl_xor(v.m, d, 64);
-        o.s = __shfl_xor(v.s, d, 64);
-        o.w = __shfl_xor(v.w, d, 64);
-        v = join(v, o, c);
-    }
-    return v;
+    v = join_step<0>(v, c);
+    v = join_step<1>(v, c);
+    v = join_step<2>(v, c);
+    v = join_step<3>(v, c);
+    v = join_step<4>(v, c);
+    return join_step<5>(v, c);
 }
 
 // The n largest keys a wave has seen, largest in lane 0.  A key is the
@@ -47,7 +48,7 @@ __device__ __forceinline__ Stats join_lanes(Stats v, float c) {
 // among equals the lower column, comes first, in whatever order keys arrive.
 struct Best {
     uint64_t list;      // lane i: the i-th largest (0: none yet)
-    uint64_t last;      // the n-th largest, the one to beat
+    uint64_t last;      // a key must be above this to enter: the n-th largest, or a lower bound of it
 };
 
 __device__ __forceinline__ uint64_t readlane64(uint64_t v, int lane) {
@@ -56,13 +57,15 @@ __device__ __forceinline__ uint64_t readlane64(uint64_t v, int lane) {
     return ((uint64_t)hi << 32) | lo;
 }
 
+// key into the sorted list: the lanes below its place move up by one
 __device__ __forceinline__ void insert(Best &b, uint64_t key, int n, int lane) {
     const int at = __builtin_popcountll(__ballot(b.list > key));
-    const uint32_t lo = (uint32_t)__shfl_up((int)(uint32_t)b.list, 1, 64);
-    const uint32_t hi = (uint32_t)__shfl_up((int)(uint32_t)(b.list >> 32), 1, 64);
+    const uint32_t lo = dpp_mov<0x138>((uint32_t)b.list);              // wave_shr:1
+    const uint32_t hi = dpp_mov<0x138>((uint32_t)(b.list >> 32));
     const uint64_t up = ((uint64_t)hi << 32) | lo;
     b.list = lane < at ? b.list : lane == at ? key : up;
-    b.last = readlane64(b.list, n - 1);
+    const uint64_t nth = readlane64(b.list, n - 1);
+    b.last = nth > b.last ? nth : b.last;
 }
 
 // every lane's key that beats the n-th so far
@@ -73,17 +76,48 @@ __device__ __forceinline__ void offer(Best &b, uint64_t key, int n, int lane) {
     }
 }
 
+// Raises the bar of an empty list to the n-th largest of one value per lane
+// (each lane holding a key with that order key at least), so that a first
+// batch of many values costs about n insertions instead of n log(values / n).
+// The value's upper 16 bits are found by bisection, one ballot a bit.
+__device__ __forceinline__ void raise(Best &b, uint32_t order, int n) {
+    uint32_t bar = 0;
+#pragma unroll
+    for (int bit = 31; bit >= 16; --bit) {
+        const uint32_t t = bar | (1u << bit);
+        if (__builtin_popcountll(__ballot(order >= t)) >= n) bar = t;
+    }
+    if (bar) b.last = ((uint64_t)bar << 32) - 1;
+}
+
+// the n largest of `count` keys (0: none) in memory
+__device__ __forceinline__ Best best_of(const uint64_t *keys, int count, int n, int lane) {
+    Best b{0, 0};
+    uint32_t order = 0;
+    for (int i = lane; i < count; i += 64) {
+        const uint32_t o = (uint32_t)(keys[i] >> 32);
+        order = o > order ? o : order;
+    }
+    raise(b, order, n);
+    for (int i = 0; i < count; i += 64) offer(b, i + lane < count ? keys[i + lane] : 0, n, lane);
+    return b;
+}
+
 __device__ __forceinline__ uint64_t logit_key(float x, int64_t col) {
     return ((uint64_t)order_key(x) << 32) | (uint32_t)~(uint32_t)col;
 }
 
-// One 16-byte piece into a lane's running statistics: one new maximum and one
-// rescaling a piece, so the maximum is exact and no term is positive.
-template <int N>
-__device__ __forceinline__ void add(Stats &v, const float *x, float c) {
-    float m = v.m;
+// N logits of every lane into its running statistics and, with TOP, the
+// wave's best list.  One new maximum and one rescaling for the N together, so
+// the maximum is exact and no term is positive.  Logit i of a lane is in
+// column col + (i / V) * step + i % V; columns from hi on hold -Inf.
+template <int N, int V, bool TOP>
+__device__ __forceinline__ void take(Stats &v, Best &best, const float *x, float c, int64_t col, int64_t step, int64_t hi,
+                                     int n, int lane) {
+    float g = x[0];
 #pragma unroll
-    for (int i = 0; i < N; ++i) m = __builtin_fmaxf(m, x[i]);
+    for (int i = 1; i < N; ++i) g = __builtin_fmaxf(g, x[i]);
+    const float m = __builtin_fmaxf(v.m, g);
     const float d = __builtin_fmaxf((v.m - m) * c, -1000.0f);
     const float f = __builtin_amdgcn_exp2f(d);
     v.w = __builtin_fmaf(v.s, d, v.w) * f;
@@ -95,6 +129,18 @@ __device__ __forceinline__ void add(Stats &v, const float *x, float c) {
         const float e = __builtin_amdgcn_exp2f(u);
         v.s += e;
         v.w = __builtin_fmaf(e, __builtin_fmaxf(u, -1000.0f), v.w);     // 0 * -Inf stays 0; a NaN is in s
+    }
+    if constexpr (TOP) {
+        // an empty list's bar is 0, the key of a NaN, which no g is below
+        if (__ballot(!(g < order_value((uint32_t)(best.last >> 32))))) {
+            if (best.last == 0) raise(best, col < hi ? order_key(g) : 0u, n);
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                if (!__ballot(!(x[i] < order_value((uint32_t)(best.last >> 32))))) continue;
+                const int64_t at = col + i / V * step + i % V;
+                offer(best, at < hi ? logit_key(x[i], at) : 0, n, lane);
+            }
+        }
     }
 }
 
@@ -135,11 +181,11 @@ __device__ __forceinline__ uint64_t *part_keys(const LogprobsArgs &a) {
 
 // One pass over a slice of a row: running maximum, sum and weighted sum per
 // lane, joined over the block.
-template <class E, bool TOP>
-__global__ __launch_bounds__(kBlock) void logprobs_kernel(const LogprobsArgs a) {
-    constexpr int kV = Elem<E>::kVec;
+template <class E, bool TOP, int BLOCK>
+__global__ __launch_bounds__(BLOCK) void logprobs_kernel(const LogprobsArgs a) {
+    constexpr int kV = Elem<E>::kVec, kWaves = BLOCK / 64;
     __shared__ Stats parts[kWaves];
-    __shared__ uint64_t keys[kWaves][TOP ? kLogprobsMaxTop : 1];
+    __shared__ uint64_t keys[TOP ? kWaves * kLogprobsMaxTop : 1];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int64_t t = (int64_t)blockIdx.x / a.slices;
     const int slice = (int)((int64_t)blockIdx.x - t * a.slices);
@@ -150,28 +196,17 @@ __global__ __launch_bounds__(kBlock) void logprobs_kernel(const LogprobsArgs a) 
     Stats v{kLowest, 0.0f, 0.0f};
     Best best{0, 0};
 
-    constexpr int kStep = kBlock * kV;
+    constexpr int kStep = BLOCK * kV;
     int64_t col = lo + threadIdx.x * kV;
     int64_t base = lo;                               // the block's position, the same in all lanes
     for (; base + kUnroll * kStep <= hi; base += kUnroll * kStep, col += kUnroll * kStep) {
         v4u r[kUnroll];
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) r[u] = load16(row + col + u * kStep);
+        float x[kUnroll * kV];
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            float x[kV];
-            Elem<E>::unpack(r[u], x);
-            add<kV>(v, x, c);
-            if constexpr (TOP) {
-                float m = x[0];
-#pragma unroll
-                for (int i = 1; i < kV; ++i) m = __builtin_fmaxf(m, x[i]);
-                if (__ballot(!(m < order_value((uint32_t)(best.last >> 32))))) {
-#pragma unroll
-                    for (int i = 0; i < kV; ++i) offer(best, logit_key(x[i], col + u * kStep + i), a.top, lane);
-                }
-            }
-        }
+        for (int u = 0; u < kUnroll; ++u) Elem<E>::unpack(r[u], x + u * kV);
+        take<kUnroll * kV, kV, TOP>(v, best, x, c, col, kStep, hi, a.top, lane);
     }
     for (; base < hi; base += kStep, col += kStep) {
         float x[kV];
@@ -182,25 +217,18 @@ __global__ __launch_bounds__(kBlock) void logprobs_kernel(const LogprobsArgs a) 
 #pragma unroll
             for (int i = 0; i < kV; ++i) x[i] = i < n ? Elem<E>::get(row[col + i]) : -__builtin_inff();
         }
-        add<kV>(v, x, c);
-        if constexpr (TOP) {
-#pragma unroll
-            for (int i = 0; i < kV; ++i) offer(best, i < n ? logit_key(x[i], col + i) : 0, a.top, lane);
-        }
+        take<kV, kV, TOP>(v, best, x, c, col, 0, hi, a.top, lane);
     }
 
     v = join_lanes(v, c);
     if (lane == 0) parts[wave] = v;
     if constexpr (TOP) {
-        if (lane < a.top) keys[wave][lane] = best.list;
+        if (lane < a.top) keys[wave * a.top + lane] = best.list;
     }
     __syncthreads();
     if (wave != 0) return;
-#pragma unroll
-    for (int w = 1; w < kWaves; ++w) {
-        v = join(v, parts[w], c);
-        if constexpr (TOP) offer(best, lane < a.top ? keys[w][lane] : 0, a.top, lane);
-    }
+    v = join_lanes(lane < kWaves ? parts[lane] : Stats{kLowest, 0.0f, 0.0f}, c);
+    if constexpr (TOP) best = best_of(keys, kWaves * a.top, a.top, lane);
     if (a.slices == 1) {
         finish_row<E>(a, t, v, best.list, lane);
     } else {
@@ -225,9 +253,8 @@ __global__ __launch_bounds__(64) void logprobs_join_kernel(const LogprobsArgs a)
     v = join_lanes(v, c);
     Best best{0, 0};
     if (a.top) {
-        const int64_t n = (int64_t)a.slices * a.top;
-        const uint64_t *keys = part_keys(a) + t * n;
-        for (int64_t i = 0; i < n; i += 64) offer(best, i + lane < n ? keys[i + lane] : 0, a.top, lane);
+        const int n = a.slices * a.top;
+        best = best_of(part_keys(a) + t * n, n, a.top, lane);
     }
     finish_row<E>(a, t, v, best.list, lane);
 }
@@ -280,11 +307,20 @@ __global__ __launch_bounds__(kBlock) void logprobs_backward_kernel(const Logprob
     }
 }
 
-// Slices of a row: enough blocks to fill the chip, at least 4096 logits each.
+// Slices of a row: one where the rows alone give every compute unit a block,
+// else enough for four blocks each, of at least 4096 logits.
 int slices_of(int64_t T, int64_t V, int cus) {
-    const int64_t want = ceil_div((int64_t)cus * 8, T), most = ceil_div(V, 4096);
-    const int64_t s = want < most ? want : most;
-    return s < 1 ? 1 : (int)s;
+    if (T >= cus) return 1;
+    const int64_t want = ceil_div((int64_t)cus * 4, T), most = ceil_div(V, 4096);
+    return (int)(want < most ? want : most);
+}
+
+template <class E, bool TOP>
+void start(const LogprobsArgs &a, hipStream_t stream) {
+    const unsigned grid = (unsigned)(a.T * a.slices);
+    if (a.slice > 16384) logprobs_kernel<E, TOP, kWide><<<grid, kWide, 0, stream>>>(a);
+    else logprobs_kernel<E, TOP, kBlock><<<grid, kBlock, 0, stream>>>(a);
+    if (a.slices > 1) logprobs_join_kernel<E><<<(unsigned)a.T, 64, 0, stream>>>(a);
 }
 
 }  // namespace
@@ -300,15 +336,12 @@ hipError_t launch_logprobs(LogprobsArgs a, bool bf16, size_t workspace_bytes, hi
     a.slices = slices_of(a.T, a.V, cus);
     if (!a.workspace || (int64_t)workspace_bytes < logprobs_workspace_bytes(a.T, a.V, a.top, cus)) a.slices = 1;
     a.slice = ceil_div(ceil_div(a.V, a.slices), 8) * 8;
-    const unsigned grid = (unsigned)(a.T * a.slices);
     if (bf16) {
-        if (a.top) logprobs_kernel<uint16_t, true><<<grid, kBlock, 0, stream>>>(a);
-        else logprobs_kernel<uint16_t, false><<<grid, kBlock, 0, stream>>>(a);
-        if (a.slices > 1) logprobs_join_kernel<uint16_t><<<(unsigned)a.T, 64, 0, stream>>>(a);
+        if (a.top) start<uint16_t, true>(a, stream);
+        else start<uint16_t, false>(a, stream);
     } else {
-        if (a.top) logprobs_kernel<float, true><<<grid, kBlock, 0, stream>>>(a);
-        else logprobs_kernel<float, false><<<grid, kBlock, 0, stream>>>(a);
-        if (a.slices > 1) logprobs_join_kernel<float><<<(unsigned)a.T, 64, 0, stream>>>(a);
+        if (a.top) start<float, true>(a, stream);
+        else start<float, false>(a, stream);
     }
     return hipGetLastError();
 }

@@ -41,19 +41,18 @@ def token_logprobs(logits: torch.Tensor, targets: torch.Tensor, *, temperature: 
     [T, V], rows contiguous, any row stride) (mxfp8_token_logprobs)."""
     code, ld, T, V = _logits_targets(logits, targets)
     L = tokens_lib()
-    dev = logits.device
-    logprobs = torch.empty(T, dtype=torch.float32, device=dev)
-    entropy = torch.empty(T, dtype=torch.float32, device=dev)
-    stats = torch.empty((T, 2), dtype=torch.float32, device=dev)
+    logprobs = logits.new_empty(T, dtype=torch.float32)
+    entropy = torch.empty_like(logprobs)
+    stats = logprobs.new_empty((T, 2))
     top = ids = None
     if top_n:
-        top = torch.empty((T, top_n), dtype=torch.float32, device=dev)
-        ids = torch.empty((T, top_n), dtype=torch.int64, device=dev)
+        top = logprobs.new_empty((T, top_n))
+        ids = targets.new_empty((T, top_n))
     need = int(L.mxfp8_token_logprobs_workspace_bytes(T, V, top_n))
-    ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    ws = logits.new_empty(need, dtype=torch.uint8) if need else None
     _check(L.mxfp8_token_logprobs(_ptr(logits), code, ld, T, V, _ptr(targets), temperature, top_n, _ptr(logprobs),
                                   _ptr(entropy), _ptr(stats), _ptr(top) if top_n else None,
-                                  _ptr(ids) if top_n else None, _ptr(ws) if need else None, need, _stream(dev)),
+                                  _ptr(ids) if top_n else None, _ptr(ws) if need else None, need, _stream(logits.device)),
            "mxfp8_token_logprobs")
     return TokenLogprobs(logprobs, entropy, stats, top, ids)
 
@@ -80,7 +79,7 @@ def token_logprobs_backward(logits: torch.Tensor, targets: torch.Tensor, stats: 
                 raise ValueError("%s must have T = %d entries" % (name, T))
     same_device(logits, stats, entropy, d_logprobs, d_entropy)
     if out is None:
-        out = torch.empty((T, V), dtype=logits.dtype, device=logits.device)
+        out = logits.new_empty((T, V))
         ld_out = V
     else:
         out_code, ld_out = need_rows(out, "out")

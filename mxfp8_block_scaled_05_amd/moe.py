@@ -47,8 +47,8 @@ def route(logits: torch.Tensor, k: int, *, score: str = "softmax", bias: torch.T
             raise ValueError("bias must have E = %d entries" % E)
         same_device(logits, bias)
     sc = _score_code(score)
-    ids = torch.empty((T, k), dtype=torch.int32, device=logits.device)
-    weights = torch.empty((T, k), dtype=torch.float32, device=logits.device)
+    ids = logits.new_empty((T, k), dtype=torch.int32)
+    weights = logits.new_empty((T, k), dtype=torch.float32)
     _check(tokens_lib().mxfp8_route(_ptr(logits), code, ld, T, E, k, sc, _ptr(bias) if bias is not None else None,
                                     groups, groups_kept, group_top, renormalize, scale, _ptr(ids), _ptr(weights),
                                     _stream(logits.device)), "mxfp8_route")
@@ -67,7 +67,7 @@ def route_backward(logits: torch.Tensor, ids: torch.Tensor, d_weights: torch.Ten
         raise ValueError("ids and d_weights must both be [T = %d, k]" % T)
     same_device(logits, ids, d_weights)
     sc = _score_code(score)
-    out = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
+    out = logits.new_empty((T, E))
     _check(tokens_lib().mxfp8_route_backward(_ptr(logits), code, ld, T, E, ids.shape[1], sc, _ptr(ids),
                                              _ptr(d_weights), renormalize, scale, _ptr(out),
                                              _stream(logits.device)), "mxfp8_route_backward")
@@ -106,10 +106,10 @@ def route_tables(ids: torch.Tensor, experts: int, pad: int = 32, rows: int | Non
                            torch.zeros(experts, dtype=torch.int32, device=dev),
                            torch.full((rows,), -1, dtype=torch.int64, device=dev),
                            torch.empty((0, k), dtype=torch.int32, device=dev), pad)
-    offsets = torch.empty(experts + 1, dtype=torch.int32, device=dev)
-    counts = torch.empty(experts, dtype=torch.int32, device=dev)
-    row_token = torch.empty(rows, dtype=torch.int64, device=dev)
-    pair_row = torch.empty((T, k), dtype=torch.int32, device=dev)
+    offsets = ids.new_empty(experts + 1)
+    counts = ids.new_empty(experts)
+    row_token = ids.new_empty(rows, dtype=torch.int64)
+    pair_row = torch.empty_like(ids)
     need = int(L.mxfp8_route_tables_workspace_bytes(T, k, experts))
     ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
     _check(L.mxfp8_route_tables(_ptr(ids), T, k, experts, pad, _ptr(offsets), _ptr(counts), _ptr(row_token), rows,
@@ -137,7 +137,7 @@ def moe_combine(y: torch.Tensor, pair_row: torch.Tensor, weights: torch.Tensor,
     T, k = pair_row.shape
     rows, H = y.shape
     if out is None:
-        out = torch.empty((T, H), dtype=y.dtype, device=y.device)
+        out = y.new_empty((T, H))
     else:
         _need(out, y.dtype, "out")
         if tuple(out.shape) != (T, H):
