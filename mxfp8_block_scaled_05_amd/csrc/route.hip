@@ -10,7 +10,8 @@ namespace {
 
 constexpr int kBlock = 256;
 
-// NV values of a lane, count of them in the row (the rest become `pad`).
+// NV values of a lane, count of them in the row (the rest become `pad`).  p is
+// readable also with count 0.
 template <int NV, class E>
 __device__ __forceinline__ void load_values(const E *p, int count, float pad, float (&x)[NV]) {
     if constexpr (NV >= Elem<E>::kVec) {
@@ -20,8 +21,12 @@ __device__ __forceinline__ void load_values(const E *p, int count, float pad, fl
             return;
         }
     }
+    // loads without a branch (one each element costs a round trip each)
+    E r[NV];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) x[i] = i < count ? Elem<E>::get(p[i]) : pad;
+    for (int i = 0; i < NV; ++i) r[i] = p[i < count ? i : 0];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) x[i] = i < count ? Elem<E>::get(r[i]) : pad;
 }
 
 // Reduction over aligned groups of 2^shift lanes, shift known at run time
@@ -92,73 +97,73 @@ __device__ __forceinline__ LaneExperts lane_experts(const RouteArgs &a, int l) {
     return e;
 }
 
-// The choice in fp64, for the tokens of a wave of which one has two
-// candidates closer than fp32 can order: the same steps as route_kernel's,
-// on 64-bit keys.  sel[j] of every token gets the j-th expert.
+// What the fp64 score of an expert needs besides its logit: for a softmax the
+// largest logit of the row and the sum of e^(x - top).
+struct Fp64Row {
+    double top, total;
+};
+template <int L, class E>
+__device__ __forceinline__ Fp64Row fp64_row(const RouteArgs &a, const E *row, const LaneExperts &ex, float top) {
+    Fp64Row r{(double)top, 1.0};
+    if (a.sigmoid || a.order_x) return r;
+    r.total = 0.0;
+#pragma unroll 1
+    for (int i = 0; i < ex.count; ++i) r.total += exp((double)Elem<E>::get(row[ex.first + i]) - r.top);
+#pragma unroll
+    for (int d = 1; d < L; d <<= 1) r.total += __shfl_xor(r.total, d, 64);
+    return r;
+}
+// the value that decides: the biased score, or the logit where that has the same order
+__device__ __forceinline__ double fp64_value(const RouteArgs &a, const Fp64Row &r, float x, int id) {
+    if (a.order_x) return x;
+    const double s = a.sigmoid ? 1.0 / (1.0 + exp(-(double)x)) : exp((double)x - r.top) / r.total;
+    return a.bias ? s + (double)a.bias[id] : s;
+}
+
+// Whether the lane's group of experts stays, with the groups' scores in fp64.
+// Only experts that may be among a group's largest are computed: those above
+// `bar` (fp32), one or two a group as a rule.
 template <int L, int NV, class E>
-__device__ __forceinline__ void choose_fp64(const RouteArgs &a, const E *row, const float *bias, int lane, int *sel) {
+__device__ __forceinline__ bool keep_fp64(const RouteArgs &a, const E *row, const LaneExperts &ex, const Fp64Row &r,
+                                          const float (&v)[NV], float bar, int lane) {
+    uint32_t some = 0;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) some |= (i < ex.count && !(v[i] < bar)) ? 1u << i : 0u;
+    double b1 = -__builtin_inf(), b2 = -__builtin_inf();
+    for (; some; some &= some - 1) {
+        const int id = ex.first + __builtin_ctz(some);
+        const double c = fp64_value(a, r, Elem<E>::get(row[id]), id);
+        const double low = c > b1 ? b1 : c;
+        b1 = c > b1 ? c : b1;
+        b2 = low > b2 ? low : b2;
+    }
+    for (int d = 1; d < (1 << a.lanes_shift); d <<= 1) {
+        const double o1 = __shfl_xor(b1, d, 64), o2 = __shfl_xor(b2, d, 64);
+        const double low = o1 < b1 ? o1 : b1, second = o2 > b2 ? o2 : b2;
+        b1 = o1 > b1 ? o1 : b1;
+        b2 = low > second ? low : second;
+    }
+    const uint64_t mine = order_key(a.group_top == 2 ? b1 + b2 : b1);
+    int rank = 0;
+    for (int g = 0; g < a.groups; ++g) {
+        const uint64_t o = shfl64(mine, (lane & ~(L - 1)) + (g << a.lanes_shift));
+        rank += (o > mine || (o == mine && g < ex.g)) ? 1 : 0;
+    }
+    return ex.g < a.groups && rank < a.kept;
+}
+
+// The whole choice in fp64, for the tokens of a wave of which one has more
+// candidates that fp32 cannot order than route_kernel's list holds (many
+// equal logits): the same steps on 64-bit keys.  sel[j] of every token gets
+// the j-th expert.
+template <int L, int NV, class E>
+__device__ __forceinline__ void choose_fp64(const RouteArgs &a, const E *row, const LaneExperts &ex, const Fp64Row &r,
+                                            bool keep, int lane, int *sel) {
     const int seg = lane & ~(L - 1), l = lane & (L - 1);
-    const LaneExperts ex = lane_experts<NV>(a, l);
     double c[NV];
-    double top = -__builtin_inf();
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        c[i] = i < ex.count ? (double)Elem<E>::get(row[ex.first + i]) : -__builtin_inf();
-        top = c[i] > top ? c[i] : top;
-    }
-    if (a.sigmoid) {
-#pragma unroll
-        for (int i = 0; i < NV; ++i) c[i] = 1.0 / (1.0 + exp(-c[i]));
-    } else {
-#pragma unroll
-        for (int d = 1; d < L; d <<= 1) {
-            const double o = __shfl_xor(top, d, 64);
-            top = o > top ? o : top;
-        }
-        double sum = 0.0;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            c[i] = i < ex.count ? exp(c[i] - top) : 0.0;
-            sum += c[i];
-        }
-#pragma unroll
-        for (int d = 1; d < L; d <<= 1) sum += __shfl_xor(sum, d, 64);
-#pragma unroll
-        for (int i = 0; i < NV; ++i) c[i] = c[i] / sum;
-    }
-    if (bias) {
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-            if (i < ex.count) c[i] += (double)bias[ex.first + i];
-    }
-    bool keep = ex.g < a.groups;
-    if (a.groups > 1) {
-        double b1 = -__builtin_inf(), b2 = -__builtin_inf();
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            if (i < ex.count) {
-                if (c[i] > b1) {
-                    b2 = b1;
-                    b1 = c[i];
-                } else if (c[i] > b2) {
-                    b2 = c[i];
-                }
-            }
-        }
-        for (int d = 1; d < (1 << a.lanes_shift); d <<= 1) {
-            const double o1 = __shfl_xor(b1, d, 64), o2 = __shfl_xor(b2, d, 64);
-            const double low = o1 < b1 ? o1 : b1, second = o2 > b2 ? o2 : b2;
-            b1 = o1 > b1 ? o1 : b1;
-            b2 = low > second ? low : second;
-        }
-        const uint64_t mine = order_key(a.group_top == 2 ? b1 + b2 : b1);
-        int rank = 0;
-        for (int g = 0; g < a.groups; ++g) {
-            const uint64_t o = shfl64(mine, seg + (g << a.lanes_shift));
-            rank += (o > mine || (o == mine && g < ex.g)) ? 1 : 0;
-        }
-        keep = keep && rank < a.kept;
-    }
+    for (int i = 0; i < NV; ++i)
+        c[i] = i < ex.count ? fp64_value(a, r, Elem<E>::get(row[ex.first + i]), ex.first + i) : 0.0;
     uint32_t left = keep ? (1u << ex.count) - 1u : 0u;    // experts of the lane still to choose from
     for (int j = 0; j < a.k; ++j) {
         uint64_t best = 0;
@@ -197,16 +202,21 @@ __device__ __forceinline__ void choose_fp64(const RouteArgs &a, const E *row, co
 // largest key below it, max((key - head) mod 2^32), which needs no marking of
 // taken experts.
 //
-// fp32 cannot order two scores that differ by less than its rounding, so
-// neighbours in the chosen order (and the last kept and first dropped group)
-// whose keys are equal, or whose scores are closer than twice their error,
-// send the wave through choose_fp64.  That error is at most 4 half steps of
-// fp32 for a sigmoid, 32 of the largest score for a softmax (half of it the
-// sum's), and one for the bias; `margin` and kRel hold the doubles.  Without a bias the order of s is that of x: bf16 logits are
-// then compared exactly (16 bits of value fit the key).
+// fp32 cannot order two scores that differ by less than its rounding.  The
+// error of a score here is at most 4 half steps of fp32 for a sigmoid, 32 of
+// the largest score for a softmax (half of it the sum's), and one for the
+// bias; `margin` holds the double of the former, kRel that of the latter and
+// of the 4 bits that a key drops.  Groups closer than that are scored again
+// in fp64 (keep_fp64).  Where neighbours of the chosen order are, the list of
+// choices is made a little longer, up to a clear gap, and sorted again by
+// fp64 values, one expert a lane (no gap: choose_fp64).  About one wave in
+// fifty takes these ways at 256 experts; without them the whole choice in
+// fp64 was 10 of 25 us at 16384 tokens.  Without a bias the order of s is that
+// of x: bf16 logits are then compared exactly (16 bits of value fit the key),
+// fp32 ones sorted again by the logit itself.
 template <int L, int NV, class E>
 __global__ __launch_bounds__(kBlock, 4) void route_kernel(const RouteArgs a) {
-    __shared__ int sel[kBlock / L][kRouteMaxK + 1];
+    __shared__ int sel[kBlock / L][L];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int seg = lane & ~(L - 1), l = lane & (L - 1);
     const int slot = wave * (64 / L) + lane / L;
@@ -216,8 +226,9 @@ __global__ __launch_bounds__(kBlock, 4) void route_kernel(const RouteArgs a) {
     const LaneExperts ex = lane_experts<NV>(a, l);
     const float kNone = -__builtin_inff();
 
-    float v[NV];
+    float v[NV], bias[NV];
     load_values<NV>(row + (ex.count ? ex.first : 0), ex.count, kNone, v);
+    if (a.bias) load_values<NV>(a.bias + (ex.count ? ex.first : 0), ex.count, 0.0f, bias);
     float top = v[0];
 #pragma unroll
     for (int i = 1; i < NV; ++i) top = __builtin_fmaxf(top, v[i]);
@@ -247,12 +258,10 @@ __global__ __launch_bounds__(kBlock, 4) void route_kernel(const RouteArgs a) {
     }
     if (a.bias) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
-            if (i < ex.count) v[i] += a.bias[ex.first + i];
+        for (int i = 0; i < NV; ++i) v[i] += bias[i];
     }
 
-    const float kRel = 0x1p-20f;
-    bool close = false;
+    const float kRel = 0x1p-18f;
     bool keep = ex.g < a.groups;
     if (a.groups > 1) {
         float b1 = kNone, b2 = kNone;
@@ -289,7 +298,12 @@ __global__ __launch_bounds__(kBlock, 4) void route_kernel(const RouteArgs a) {
         if (!a.order_x) {
             const float low = group_reduce<L>(keep ? score : __builtin_inff(), OpMin());
             const float high = group_reduce<L>(in && !keep ? score : kNone, OpMax());
-            close = !(low - high > 2.0f * margin + kRel * (__builtin_fabsf(low) + __builtin_fabsf(high)));
+            const bool close = !(low - high > 2.0f * margin + kRel * (__builtin_fabsf(low) + __builtin_fabsf(high)));
+            if (__ballot(close && live)) {
+                const float bar = a.group_top == 2 ? b2 : b1;
+                keep = keep_fp64<L, NV, E>(a, row, ex, fp64_row<L, E>(a, row, ex, top), v,
+                                           bar - (2.0f * margin + kRel * __builtin_fabsf(bar)), lane);
+            }
         }
     }
 
@@ -303,28 +317,35 @@ __global__ __launch_bounds__(kBlock, 4) void route_kernel(const RouteArgs a) {
         head = key[i] > head ? key[i] : head;
     }
     uint32_t mine = 0;                             // lane j: the j-th largest key
-    const int rounds = a.k + (a.order_exact ? 0 : 1);
-    for (int j = 0; j < rounds; ++j) {
-        const uint32_t hv = head & ~15u;
-        const uint32_t M = group_reduce<L>(hv, OpMax());
-        const int own = first_lane<L>(__ballot(hv == M), seg);
-        if (l == j) mine = M;
-        if (l == own) {
-            sel[slot][j] = ex.first + 15 - (int)(head & 15u);
-            uint32_t d = 0u - head;
+    // choices j0 .. j1 - 1 of every token
+    auto choose = [&](int j0, int j1) {
+        for (int j = j0; j < j1; ++j) {
+            const uint32_t hv = head & ~15u;
+            const uint32_t M = group_reduce<L>(hv, OpMax());
+            const int own = first_lane<L>(__ballot(hv == M), seg);
+            if (l == j) mine = M;
+            if (l == own) {
+                sel[slot][j] = ex.first + 15 - (int)(head & 15u);
+                uint32_t d = 0u - head;
 #pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const uint32_t e = key[i] - head;
-                d = e > d ? e : d;
+                for (int i = 0; i < NV; ++i) {
+                    const uint32_t e = key[i] - head;
+                    d = e > d ? e : d;
+                }
+                head += d;
             }
-            head += d;
         }
-    }
-    wave_sync();
-    const int count = rounds < a.candidates ? rounds : a.candidates;       // entries of sel that are experts
-    int id = l < count ? sel[slot][l] : 0;
-    float x = Elem<E>::get(row[id]);
-    if (!a.order_exact) {
+        wave_sync();
+    };
+    // the logit of the listed expert of the lane, and whether its place before
+    // the next lane's is beyond doubt
+    int count = a.k + (a.order_exact || a.k == a.candidates ? 0 : 1);
+    int id = 0;
+    float x = 0.0f;
+    auto listed = [&]() {
+        id = l < count ? sel[slot][l] : 0;
+        x = Elem<E>::get(row[id]);
+        if (a.order_exact) return true;
         float c = x;
         if (!a.order_x) {
             c = a.sigmoid ? fast_sigmoid(x) : __builtin_amdgcn_exp2f((x - top) * kLog2E) * inv;
@@ -332,16 +353,36 @@ __global__ __launch_bounds__(kBlock, 4) void route_kernel(const RouteArgs a) {
         }
         const uint32_t next = (uint32_t)__shfl_down((int)mine, 1, 64);
         const float below = __shfl_down(c, 1, 64);
-        if (l + 1 < count) {
-            close = close || mine == next;
-            if (!a.order_x) close = close || !(c - below > margin + kRel * __builtin_fabsf(c));
-        }
-        if (__ballot(close && live)) {
-            choose_fp64<L, NV, E>(a, row, a.bias, lane, sel[slot]);
+        return mine != next && (a.order_x || c - below > margin + kRel * __builtin_fabsf(c));
+    };
+    choose(0, count);
+    bool clear = listed();
+    if (__ballot(!clear && l + 1 < count && live)) {
+        const int more = a.candidates < L ? a.candidates : L;
+        const int longer = count + 3 < more ? count + 3 : more;
+        choose(count, longer);
+        count = longer;
+        clear = listed();
+        // lanes of the token whose place ends a list that holds every contender for the k
+        const uint64_t ends = __ballot(clear && l >= a.k - 1 && l + 1 < count);
+        const bool whole = count == a.candidates || first_lane<L>(ends, seg) < L;
+        const Fp64Row r = fp64_row<L, E>(a, row, ex, top);
+        if (__ballot(!whole && live)) {
+            choose_fp64<L, NV, E>(a, row, ex, r, keep, lane, sel[slot]);
+        } else {
+            uint64_t value = order_key(fp64_value(a, r, x, id));
+            int rank = 0;
+            for (int j = 0; j < count; ++j) {
+                const uint64_t o = shfl64(value, seg + j);
+                const int other = __shfl(id, seg + j, 64);
+                rank += (o > value || (o == value && other < id)) ? 1 : 0;
+            }
             wave_sync();
-            id = l < a.k ? sel[slot][l] : 0;
-            x = Elem<E>::get(row[id]);
+            if (l < count && rank < a.k) sel[slot][rank] = id;
         }
+        wave_sync();
+        id = l < a.k ? sel[slot][l] : 0;
+        x = Elem<E>::get(row[id]);
     }
 
     float w = 0.0f;
