@@ -1,5 +1,7 @@
 // Log-probabilities of given tokens, entropy and the likeliest tokens of rows
 // of logits, and the gradient of the first two.
+#include <type_traits>
+
 #include "mx_launch.hpp"
 #include "mx_wave.hpp"
 
@@ -8,7 +10,13 @@ namespace mx {
 namespace {
 
 constexpr int kBlock = 256;         // threads of the gradient's and of split rows' blocks
-constexpr int kWide = 1024;         // threads of a block that has a long row to itself
+// Threads of a block that has a long row to itself: 1024 (2048 rows of 131072
+// bf16: 95.0 us, with 512 99.0, with 256 101.5), or 512 where it also looks
+// for the best n, whose steps are short and in sequence, so that another
+// block of the unit can stream meanwhile (same rows, n = 5: 108.0 us, with
+// 1024 141.7, with 256 110.2; 511 rows of 100003 fp32: 38.7, 43.9, 39.5).
+constexpr int kWide = 1024;
+constexpr int kWideTop = 512;
 constexpr int kUnroll = 4;          // 16-byte loads of a thread in flight
 constexpr float kLowest = -3.402823466e38f;
 
@@ -49,12 +57,19 @@ __device__ __forceinline__ Stats join_lanes(Stats v, float c) {
 struct Best {
     uint64_t list;      // lane i: the i-th largest (0: none yet)
     uint64_t last;      // a key must be above this to enter: the n-th largest, or a lower bound of it
+    int have;           // entries of the list, at most n
+    uint64_t *room;     // LDS of the wave: 64 keys
 };
 
 __device__ __forceinline__ uint64_t readlane64(uint64_t v, int lane) {
     const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)v, lane);
     const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(v >> 32), lane);
     return ((uint64_t)hi << 32) | lo;
+}
+
+__device__ __forceinline__ void new_bar(Best &b, int n) {
+    const uint64_t nth = readlane64(b.list, n - 1);
+    b.last = nth > b.last ? nth : b.last;
 }
 
 // key into the sorted list: the lanes below its place move up by one
@@ -64,11 +79,11 @@ __device__ __forceinline__ void insert(Best &b, uint64_t key, int n, int lane) {
     const uint32_t hi = dpp_mov<0x138>((uint32_t)(b.list >> 32));
     const uint64_t up = ((uint64_t)hi << 32) | lo;
     b.list = lane < at ? b.list : lane == at ? key : up;
-    const uint64_t nth = readlane64(b.list, n - 1);
-    b.last = nth > b.last ? nth : b.last;
+    b.have = b.have < n ? b.have + 1 : n;
+    new_bar(b, n);
 }
 
-// every lane's key that beats the n-th so far
+// every lane's key that beats the n-th so far, one after another
 __device__ __forceinline__ void offer(Best &b, uint64_t key, int n, int lane) {
     for (uint64_t m = __ballot(key > b.last); m; m &= m - 1) {
         const uint64_t k = readlane64(key, __builtin_ctzll(m));
@@ -76,44 +91,100 @@ __device__ __forceinline__ void offer(Best &b, uint64_t key, int n, int lane) {
     }
 }
 
-// Raises the bar of an empty list to the n-th largest of one value per lane
-// (each lane holding a key with that order key at least), so that a first
-// batch of many values costs about n insertions instead of n log(values / n).
-// The value's upper 16 bits are found by bisection, one ballot a bit.
-__device__ __forceinline__ void raise(Best &b, uint32_t order, int n) {
-    uint32_t bar = 0;
-#pragma unroll
-    for (int bit = 31; bit >= 16; --bit) {
-        const uint32_t t = bar | (1u << bit);
-        if (__builtin_popcountll(__ballot(order >= t)) >= n) bar = t;
+// Many keys at once: those above the bar are laid down in the wave's room
+// beside the list (gather), and all of them ranked together (settle), each
+// lane counting the keys above its own.  An insertion is a chain of about 25
+// dependent steps; ranking 40 keys costs as much as four of them.
+__device__ __forceinline__ int gather_begin(const Best &b, int lane) {
+    if (lane < b.have) b.room[lane] = b.list;
+    return b.have;
+}
+__device__ __forceinline__ void settle(Best &b, int held, int n, int lane) {
+    wave_sync();
+    const uint64_t mine = lane < held ? b.room[lane] : 0;
+    int rank = 0;
+    for (int j = 0; j < held; ++j) rank += readlane64(mine, j) > mine ? 1 : 0;
+    wave_sync();
+    if (lane < held) b.room[rank] = mine;                // keys differ, so ranks do
+    wave_sync();
+    b.have = held < n ? held : n;
+    b.list = lane < b.have ? b.room[lane] : 0;
+    new_bar(b, n);
+}
+__device__ __forceinline__ void gather(Best &b, int &held, uint64_t key, int n, int lane) {
+    uint64_t m = __ballot(key > b.last);
+    if (!m) return;
+    if (held + __builtin_popcountll(m) > 64) {           // full: what is there first
+        settle(b, held, n, lane);
+        held = b.have;
+        m = __ballot(key > b.last);
+        if (held + __builtin_popcountll(m) > 64) {
+            offer(b, key, n, lane);
+            held = gather_begin(b, lane);
+            return;
+        }
     }
-    if (bar) b.last = ((uint64_t)bar << 32) - 1;
+    const int below = __builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0));
+    if ((m >> lane) & 1) b.room[held + below] = key;
+    held += __builtin_popcountll(m);
 }
 
-// the n largest of `count` keys (0: none) in memory
-__device__ __forceinline__ Best best_of(const uint64_t *keys, int count, int n, int lane) {
-    Best b{0, 0};
-    uint32_t order = 0;
-    for (int i = lane; i < count; i += 64) {
-        const uint32_t o = (uint32_t)(keys[i] >> 32);
-        order = o > order ? o : order;
+// A bar that n of the wave's values reach (N a lane): the n-th largest, its
+// upper 16 bits, by bisection.
+template <int N>
+__device__ __forceinline__ uint32_t bar_of(const uint32_t (&order)[N], int n) {
+    uint32_t bar = 0;
+    for (int bit = 31; bit >= 16; --bit) {
+        const uint32_t t = bar | (1u << bit);
+        int count = 0;
+#pragma unroll
+        for (int i = 0; i < N; ++i) count += __builtin_popcountll(__ballot(order[i] >= t));
+        if (count >= n) bar = t;
     }
-    raise(b, order, n);
-    for (int i = 0; i < count; i += 64) offer(b, i + lane < count ? keys[i + lane] : 0, n, lane);
+    return bar;
+}
+// the last key below every key of order `bar` or more
+__device__ __forceinline__ uint64_t below_bar(uint32_t bar) { return bar ? ((uint64_t)bar << 32) - 1 : 0; }
+
+// The n largest of `count` keys (0: none) in memory that are above last.  With
+// no such bar known (last = 0) the first keys give one.
+template <int AHEAD>
+__device__ __forceinline__ Best best_of(const uint64_t *keys, int count, int n, uint64_t last, uint64_t *room, int lane) {
+    Best b{0, last, 0, room};
+    int held = 0;
+    for (int i0 = 0; i0 < count; i0 += 64 * AHEAD) {
+        uint64_t k[AHEAD];
+#pragma unroll
+        for (int u = 0; u < AHEAD; ++u) {
+            const int i = i0 + u * 64 + lane;
+            k[u] = keys[i < count ? i : 0];
+            if (i >= count) k[u] = 0;
+        }
+        if (i0 == 0 && last == 0) {
+            uint32_t order[1] = {0};
+#pragma unroll
+            for (int u = 0; u < AHEAD; ++u) order[0] = (uint32_t)(k[u] >> 32) > order[0] ? (uint32_t)(k[u] >> 32) : order[0];
+            b.last = below_bar(bar_of(order, n));
+        }
+#pragma unroll
+        for (int u = 0; u < AHEAD; ++u)
+            if (i0 + u * 64 < count) gather(b, held, k[u], n, lane);
+    }
+    settle(b, held, n, lane);
     return b;
 }
 
+// Unsigned order of a logit among a row's best: a NaN above all.
+__device__ __forceinline__ uint32_t logit_order(float x) { return x != x ? 0xFFFFFFFFu : order_key(x); }
 __device__ __forceinline__ uint64_t logit_key(float x, int64_t col) {
-    return ((uint64_t)order_key(x) << 32) | (uint32_t)~(uint32_t)col;
+    return ((uint64_t)logit_order(x) << 32) | (uint32_t)~(uint32_t)col;
 }
 
-// N logits of every lane into its running statistics and, with TOP, the
-// wave's best list.  One new maximum and one rescaling for the N together, so
-// the maximum is exact and no term is positive.  Logit i of a lane is in
-// column col + (i / V) * step + i % V; columns from hi on hold -Inf.
-template <int N, int V, bool TOP>
-__device__ __forceinline__ void take(Stats &v, Best &best, const float *x, float c, int64_t col, int64_t step, int64_t hi,
-                                     int n, int lane) {
+// N logits of every lane into its running statistics; returns their maximum.
+// One new maximum and one rescaling for the N together, so the maximum is
+// exact and no term is positive.
+template <int N>
+__device__ __forceinline__ float take(Stats &v, const float *x, float c) {
     float g = x[0];
 #pragma unroll
     for (int i = 1; i < N; ++i) g = __builtin_fmaxf(g, x[i]);
@@ -130,45 +201,54 @@ __device__ __forceinline__ void take(Stats &v, Best &best, const float *x, float
         v.s += e;
         v.w = __builtin_fmaf(e, __builtin_fmaxf(u, -1000.0f), v.w);     // 0 * -Inf stays 0; a NaN is in s
     }
-    if constexpr (TOP) {
-        // an empty list's bar is 0, the key of a NaN, which no g is below
-        if (__ballot(!(g < order_value((uint32_t)(best.last >> 32))))) {
-            if (best.last == 0) raise(best, col < hi ? order_key(g) : 0u, n);
+    return g;
+}
+
+// n logits of type E at p (all of kV, or the first n and -Inf)
+template <class E>
+__device__ __forceinline__ void load_logits(const E *p, int64_t n, float *x) {
+    constexpr int kV = Elem<E>::kVec;
+    if (n >= kV) {
+        Elem<E>::unpack(load16(p), x);
+    } else {
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-                if (!__ballot(!(x[i] < order_value((uint32_t)(best.last >> 32))))) continue;
-                const int64_t at = col + i / V * step + i % V;
-                offer(best, at < hi ? logit_key(x[i], at) : 0, n, lane);
-            }
-        }
+        for (int i = 0; i < kV; ++i) x[i] = i < n ? Elem<E>::get(p[i]) : -__builtin_inff();
     }
+}
+
+// The target of a row and its logit, asked for at the start of a kernel: two
+// loads in a row, which would otherwise wait at its end.
+struct Target {
+    bool real;
+    float x;
+};
+template <class E>
+__device__ __forceinline__ Target load_target(const LogprobsArgs &a, int64_t t) {
+    const int64_t v = a.targets[t];
+    const bool real = v >= 0 && v < a.V;
+    return {real, Elem<E>::get(static_cast<const E *>(a.x)[t * a.ld + (real ? v : 0)])};
 }
 
 // Writes a row's results; the whole wave, with the joined statistics.  What
 // divides by the temperature is computed in fp64 and rounded once: a row has
 // few such values, and the quotients of two logits would otherwise each
 // round at their own size instead of that of their distance.
-template <class E>
-__device__ __forceinline__ void finish_row(const LogprobsArgs &a, int64_t t, const Stats &v, uint64_t list, int lane) {
-    const E *row = static_cast<const E *>(a.x) + t * a.ld;
+__device__ __forceinline__ void finish_row(const LogprobsArgs &a, int64_t t, const Stats &v, const Target &target,
+                                           uint64_t list, int lane) {
     const bool none = v.s == 0.0f;                       // every logit -Inf
     float top = none ? -__builtin_inff() : v.m;
     if (v.s != v.s && !(v.m > -kLowest)) top = v.s;      // a NaN among the logits
     const float log_sum = none ? __builtin_nanf("") : logf(v.s);
     if (lane == 0) {
-        const int64_t target = a.targets[t];
-        float lp = 0.0f;
-        if (target >= 0 && target < a.V)
-            lp = (float)(((double)Elem<E>::get(row[target]) - top) / a.temperature - log_sum);
-        a.logprobs[t] = lp;
+        a.logprobs[t] = target.real ? (float)(((double)target.x - top) * a.inv_temperature - log_sum) : 0.0f;
         a.entropy[t] = none ? __builtin_nanf("") : log_sum - v.w / v.s * kLn2;
-        a.stats[2 * t] = (float)(top / a.temperature);
+        a.stats[2 * t] = (float)(top * a.inv_temperature);
         a.stats[2 * t + 1] = log_sum;
     }
     if (lane < a.top) {
         a.top_ids[t * a.top + lane] = (uint32_t)~(uint32_t)list;
         const double x = order_value((uint32_t)(list >> 32));
-        a.top_logprobs[t * a.top + lane] = (float)((x - top) / a.temperature - log_sum);
+        a.top_logprobs[t * a.top + lane] = (float)((x - top) * a.inv_temperature - log_sum);
     }
 }
 
@@ -181,11 +261,19 @@ __device__ __forceinline__ uint64_t *part_keys(const LogprobsArgs &a) {
 
 // One pass over a slice of a row: running maximum, sum and weighted sum per
 // lane, joined over the block.
+//
+// The best n: the pass keeps each thread's largest logit only.  n threads'
+// largest reach the n-th largest of them, so no logit below that bar is among
+// the best, and few threads hold one above it: their logits alone are looked
+// at again (n / BLOCK of the row), those above the bar gathered and ranked.
 template <class E, bool TOP, int BLOCK>
 __global__ __launch_bounds__(BLOCK) void logprobs_kernel(const LogprobsArgs a) {
     constexpr int kV = Elem<E>::kVec, kWaves = BLOCK / 64;
     __shared__ Stats parts[kWaves];
     __shared__ uint64_t keys[TOP ? kWaves * kLogprobsMaxTop : 1];
+    __shared__ uint64_t room[TOP ? kWaves : 1][64];
+    __shared__ uint32_t largest[TOP ? BLOCK : 1];
+    __shared__ uint32_t shared_bar;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int64_t t = (int64_t)blockIdx.x / a.slices;
     const int slice = (int)((int64_t)blockIdx.x - t * a.slices);
@@ -193,57 +281,98 @@ __global__ __launch_bounds__(BLOCK) void logprobs_kernel(const LogprobsArgs a) {
     const int64_t hi = lo + a.slice < a.V ? lo + a.slice : a.V;
     const E *row = static_cast<const E *>(a.x) + t * a.ld;
     const float c = a.scale;
+    Target target{false, 0.0f};
+    if (wave == 0 && a.slices == 1) target = load_target<E>(a, t);
     Stats v{kLowest, 0.0f, 0.0f};
-    Best best{0, 0};
+    float most = -__builtin_inff();
 
     constexpr int kStep = BLOCK * kV;
     int64_t col = lo + threadIdx.x * kV;
     int64_t base = lo;                               // the block's position, the same in all lanes
-    for (; base + kUnroll * kStep <= hi; base += kUnroll * kStep, col += kUnroll * kStep) {
-        v4u r[kUnroll];
+    auto steps = [&](auto unroll) {                  // that many loads in flight, and one rescaling for them
+        constexpr int U = decltype(unroll)::value;
+        for (; base + U * kStep <= hi; base += U * kStep, col += U * kStep) {
+            v4u r[U];
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) r[u] = load16(row + col + u * kStep);
-        float x[kUnroll * kV];
+            for (int u = 0; u < U; ++u) r[u] = load16(row + col + u * kStep);
+            float x[U * kV];
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) Elem<E>::unpack(r[u], x + u * kV);
-        take<kUnroll * kV, kV, TOP>(v, best, x, c, col, kStep, hi, a.top, lane);
-    }
+            for (int u = 0; u < U; ++u) Elem<E>::unpack(r[u], x + u * kV);
+            most = __builtin_fmaxf(most, take<U * kV>(v, x, c));
+        }
+    };
+    steps(std::integral_constant<int, kUnroll>());
+    steps(std::integral_constant<int, kUnroll / 2>());
     for (; base < hi; base += kStep, col += kStep) {
         float x[kV];
-        const int64_t n = hi - col;
-        if (n >= kV) {
-            Elem<E>::unpack(load16(row + col), x);
-        } else {
-#pragma unroll
-            for (int i = 0; i < kV; ++i) x[i] = i < n ? Elem<E>::get(row[col + i]) : -__builtin_inff();
-        }
-        take<kV, kV, TOP>(v, best, x, c, col, 0, hi, a.top, lane);
+        load_logits(row + col, hi - col, x);
+        most = __builtin_fmaxf(most, take<kV>(v, x, c));
     }
 
     v = join_lanes(v, c);
     if (lane == 0) parts[wave] = v;
-    if constexpr (TOP) {
-        if (lane < a.top) keys[wave * a.top + lane] = best.list;
-    }
+    const uint32_t mine = order_key(most);
+    if constexpr (TOP) largest[threadIdx.x] = mine;
     __syncthreads();
-    if (wave != 0) return;
-    v = join_lanes(lane < kWaves ? parts[lane] : Stats{kLowest, 0.0f, 0.0f}, c);
-    if constexpr (TOP) best = best_of(keys, kWaves * a.top, a.top, lane);
-    if (a.slices == 1) {
-        finish_row<E>(a, t, v, best.list, lane);
-    } else {
-        if (lane == 0) part_stats(a)[blockIdx.x] = make_float4(v.m, v.s, v.w, 0.0f);
-        if constexpr (TOP) {
+    if constexpr (TOP) {
+        if (wave == 0) {
+            uint32_t order[kWaves];
+#pragma unroll
+            for (int i = 0; i < kWaves; ++i) order[i] = largest[i * 64 + lane];
+            const uint32_t bar = bar_of(order, a.top);
+            if (lane == 0) shared_bar = bar;
+        }
+        __syncthreads();
+        const uint64_t last = below_bar(shared_bar);
+        Best best{0, last, 0, room[wave]};
+        int held = 0;
+        // 2^shift lanes look at the pieces of one thread, `at` the first column of piece 0
+        const int pieces = (int)((hi - lo + kStep - 1) / kStep);
+        int shift = 0;
+        while (shift < 6 && (1 << shift) < pieces) ++shift;
+        for (uint64_t m = __ballot(mine >= shared_bar); m;) {
+            int from = -1;
+            for (int q = 0; q < 64 >> shift && m; ++q, m &= m - 1)
+                if (lane >> shift == q) from = __builtin_ctzll(m);
+            for (int piece = 0; piece < pieces; piece += 64) {
+                const int mypiece = piece + (lane & ((1 << shift) - 1));
+                const int64_t at = lo + (wave * 64 + from) * kV + (int64_t)mypiece * kStep;
+                const int64_t n = from >= 0 ? hi - at : 0;
+                float x[kV];
+                load_logits(row + at, n, x);
+#pragma unroll
+                for (int i = 0; i < kV; ++i) gather(best, held, i < n ? logit_key(x[i], at + i) : 0, a.top, lane);
+            }
+        }
+        wave_sync();
+        if (best.have || held > a.top) settle(best, held, a.top, lane);
+        else best.list = lane < held ? room[wave][lane] : 0;            // in any order: they are ranked below
+        if (lane < a.top) keys[wave * a.top + lane] = best.list;
+        __syncthreads();
+        if (wave != 0) return;
+        best = best_of<4>(keys, kWaves * a.top, a.top, last, room[0], lane);
+        v = join_lanes(lane < kWaves ? parts[lane] : Stats{kLowest, 0.0f, 0.0f}, c);
+        if (a.slices == 1) {
+            finish_row(a, t, v, target, best.list, lane);
+        } else {
+            if (lane == 0) part_stats(a)[blockIdx.x] = make_float4(v.m, v.s, v.w, 0.0f);
             if (lane < a.top) part_keys(a)[(int64_t)blockIdx.x * a.top + lane] = best.list;
         }
+    } else {
+        if (wave != 0) return;
+        v = join_lanes(lane < kWaves ? parts[lane] : Stats{kLowest, 0.0f, 0.0f}, c);
+        if (a.slices == 1) finish_row(a, t, v, target, 0, lane);
+        else if (lane == 0) part_stats(a)[blockIdx.x] = make_float4(v.m, v.s, v.w, 0.0f);
     }
 }
 
 // Joins the slices of a row, one wave a row.
 template <class E>
 __global__ __launch_bounds__(64) void logprobs_join_kernel(const LogprobsArgs a) {
+    __shared__ uint64_t room[64];
     const int lane = threadIdx.x;
     const int64_t t = blockIdx.x;
+    const Target target = load_target<E>(a, t);
     const float c = a.scale;
     Stats v{kLowest, 0.0f, 0.0f};
     for (int s = lane; s < a.slices; s += 64) {
@@ -251,12 +380,13 @@ __global__ __launch_bounds__(64) void logprobs_join_kernel(const LogprobsArgs a)
         v = join(v, Stats{p.x, p.y, p.z}, c);
     }
     v = join_lanes(v, c);
-    Best best{0, 0};
+    uint64_t list = 0;
     if (a.top) {
         const int n = a.slices * a.top;
-        best = best_of(part_keys(a) + t * n, n, a.top, lane);
+        const uint64_t *keys = part_keys(a) + t * n;
+        list = best_of<12>(keys, n, a.top, 0, room, lane).list;
     }
-    finish_row<E>(a, t, v, best.list, lane);
+    finish_row(a, t, v, target, list, lane);
 }
 
 // d logits = (g (1[target] - p) - h p (log p + H)) / temp with g, h the
@@ -318,7 +448,8 @@ int slices_of(int64_t T, int64_t V, int cus) {
 template <class E, bool TOP>
 void start(const LogprobsArgs &a, hipStream_t stream) {
     const unsigned grid = (unsigned)(a.T * a.slices);
-    if (a.slice > 16384) logprobs_kernel<E, TOP, kWide><<<grid, kWide, 0, stream>>>(a);
+    constexpr int wide = TOP ? kWideTop : kWide;
+    if (a.slice > 16384) logprobs_kernel<E, TOP, wide><<<grid, wide, 0, stream>>>(a);
     else logprobs_kernel<E, TOP, kBlock><<<grid, kBlock, 0, stream>>>(a);
     if (a.slices > 1) logprobs_join_kernel<E><<<(unsigned)a.T, 64, 0, stream>>>(a);
 }
@@ -332,7 +463,8 @@ int64_t logprobs_workspace_bytes(int64_t T, int64_t V, int top, int cus) {
 
 hipError_t launch_logprobs(LogprobsArgs a, bool bf16, size_t workspace_bytes, hipStream_t stream) {
     const int cus = device_cu_count();
-    a.scale = (float)(1.4426950408889634 / a.temperature);
+    a.inv_temperature = 1.0 / a.temperature;
+    a.scale = (float)(1.4426950408889634 * a.inv_temperature);
     a.slices = slices_of(a.T, a.V, cus);
     if (!a.workspace || (int64_t)workspace_bytes < logprobs_workspace_bytes(a.T, a.V, a.top, cus)) a.slices = 1;
     a.slice = ceil_div(ceil_div(a.V, a.slices), 8) * 8;
@@ -347,8 +479,9 @@ hipError_t launch_logprobs(LogprobsArgs a, bool bf16, size_t workspace_bytes, hi
 }
 
 hipError_t launch_logprobs_backward(LogprobsArgs a, bool bf16, hipStream_t stream) {
-    a.inv = (float)(1.0 / a.temperature);
-    a.inv_low = (float)(1.0 / a.temperature - a.inv);
+    a.inv_temperature = 1.0 / a.temperature;
+    a.inv = (float)a.inv_temperature;
+    a.inv_low = (float)(a.inv_temperature - a.inv);
     a.slice = 4 * kBlock * (bf16 ? 8 : 4);
     a.slices = (int)ceil_div(a.V, a.slice);
     const unsigned grid = (unsigned)(a.T * a.slices);

@@ -238,6 +238,7 @@ struct LogprobsArgs {
     void *dx;                               // [T][ld_out]
     int64_t ld_out;
     // set by the launcher
+    double inv_temperature;
     float scale, inv, inv_low;              // log2(e) / temperature; 1 / temperature in two parts
     int64_t slice;
     int slices;

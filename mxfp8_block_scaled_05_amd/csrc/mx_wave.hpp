@@ -63,6 +63,12 @@ __device__ __forceinline__ T group_reduce(T v, Op op) {
     return v;
 }
 
+// LDS written by a lane, read by another of its wave
+__device__ __forceinline__ void wave_sync() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
 // ---------------------------------------------------------------- vector access
 
 // 16 bytes at any element-aligned address: gfx950's global loads and stores

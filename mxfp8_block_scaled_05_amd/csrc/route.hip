@@ -70,12 +70,6 @@ __device__ __forceinline__ int first_lane(uint64_t b, int seg) {
     }
 }
 
-// LDS written by a lane, read by another of its wave
-__device__ __forceinline__ void wave_sync() {
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-}
-
 // 1 / (1 + e^-x) for the choice: 2^x and 1/x of the hardware
 __device__ __forceinline__ float fast_sigmoid(float x) {
     return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(x * -kLog2E));
