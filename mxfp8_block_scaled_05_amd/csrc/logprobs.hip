@@ -9,14 +9,7 @@ namespace mx {
 
 namespace {
 
-constexpr int kBlock = 256;         // threads of the gradient's and of split rows' blocks
-// Threads of a block that has a long row to itself: 1024 (2048 rows of 131072
-// bf16: 95.0 us, with 512 99.0, with 256 101.5), or 512 where it also looks
-// for the best n, whose steps are short and in sequence, so that another
-// block of the unit can stream meanwhile (same rows, n = 5: 108.0 us, with
-// 1024 141.7, with 256 110.2; 511 rows of 100003 fp32: 38.7, 43.9, 39.5).
-constexpr int kWide = 1024;
-constexpr int kWideTop = 512;
+constexpr int kBlock = 256;         // threads of the gradient's blocks
 constexpr int kUnroll = 4;          // 16-byte loads of a thread in flight
 constexpr float kLowest = -3.402823466e38f;
 
@@ -445,12 +438,25 @@ int slices_of(int64_t T, int64_t V, int cus) {
     return (int)(want < most ? want : most);
 }
 
+// Threads of a block, from the length of its slice, the rows and whether it
+// looks for the best n (whose steps are short and in sequence: smaller blocks
+// let another block of the unit stream meanwhile).  us with 64 / 128 / 256 /
+// 512 / 1024 threads:
+//   8000 rows of 1001 bf16            9.7 / 12.1 / 18.2 / 30.6 / 56.8
+//   the same with n = 5              15.8 / 20.8 / 32.6 / 82.4 / 224
+//   8000 rows of 8001 bf16, n = 5    38.9 / 36.7 / 47.6 / 90.8 / 230
+//   300 rows of 16001 bf16            8.7 /  7.6 /  6.2 /  6.3 /  7.1
+//   2600 rows of 50001 bf16          50.7 / 50.7 / 48.9 / 51.4 / 59.7
+//   1340 rows of 100003 fp32          105 /  104 /  104 / 98.6 / 96.2
+//   1340 rows of 100003 bf16, n = 5  91.7 / 68.1 / 59.3 / 57.4 / 91.3
 template <class E, bool TOP>
-void start(const LogprobsArgs &a, hipStream_t stream) {
+void start(const LogprobsArgs &a, int cus, hipStream_t stream) {
     const unsigned grid = (unsigned)(a.T * a.slices);
-    constexpr int wide = TOP ? kWideTop : kWide;
-    if (a.slice > 16384) logprobs_kernel<E, TOP, wide><<<grid, wide, 0, stream>>>(a);
-    else logprobs_kernel<E, TOP, kBlock><<<grid, kBlock, 0, stream>>>(a);
+    const bool many = a.T >= 4 * cus;
+    if (many && a.slice <= 2048) logprobs_kernel<E, TOP, 64><<<grid, 64, 0, stream>>>(a);
+    else if (many && a.slice <= 8192) logprobs_kernel<E, TOP, 128><<<grid, 128, 0, stream>>>(a);
+    else if (a.slice <= (TOP ? 32768 : 65536)) logprobs_kernel<E, TOP, 256><<<grid, 256, 0, stream>>>(a);
+    else logprobs_kernel<E, TOP, TOP ? 512 : 1024><<<grid, TOP ? 512 : 1024, 0, stream>>>(a);
     if (a.slices > 1) logprobs_join_kernel<E><<<(unsigned)a.T, 64, 0, stream>>>(a);
 }
 
@@ -469,11 +475,11 @@ hipError_t launch_logprobs(LogprobsArgs a, bool bf16, size_t workspace_bytes, hi
     if (!a.workspace || (int64_t)workspace_bytes < logprobs_workspace_bytes(a.T, a.V, a.top, cus)) a.slices = 1;
     a.slice = ceil_div(ceil_div(a.V, a.slices), 8) * 8;
     if (bf16) {
-        if (a.top) start<uint16_t, true>(a, stream);
-        else start<uint16_t, false>(a, stream);
+        if (a.top) start<uint16_t, true>(a, cus, stream);
+        else start<uint16_t, false>(a, cus, stream);
     } else {
-        if (a.top) start<float, true>(a, stream);
-        else start<float, false>(a, stream);
+        if (a.top) start<float, true>(a, cus, stream);
+        else start<float, false>(a, cus, stream);
     }
     return hipGetLastError();
 }
