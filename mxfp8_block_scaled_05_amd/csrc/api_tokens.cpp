@@ -83,8 +83,7 @@ int64_t mxfp8_route_rows(int64_t pairs, int64_t E, int64_t pad) {
 
 size_t mxfp8_route_tables_workspace_bytes(int64_t T, int64_t k, int64_t E) {
     if (T < 1 || k < 1 || T >= kMaxInt || !product_ok(T, k) || E < 1 || E > kTablesMaxExperts) return 0;
-    const int64_t chunks = ceil_div(T * k, route_tables_chunk(T * k));
-    return chunks > 1 ? (size_t)(chunks * E * 4) : 0;
+    return (size_t)route_tables_workspace_bytes(T * k, E);
 }
 
 mxfp8_status mxfp8_route_tables(const int32_t *ids, int64_t T, int64_t k, int64_t E, int64_t pad,

@@ -17,8 +17,7 @@ __device__ __forceinline__ v4u load_piece(const E *p, int n) {
     constexpr int kV = Elem<E>::kVec;
     if (n >= kV) return load16(p);
     float f[kV];
-#pragma unroll
-    for (int i = 0; i < kV; ++i) f[i] = i < n ? Elem<E>::get(p[i]) : 0.0f;
+    load_head<kV>(p, n, 0.0f, f);
     return Elem<E>::pack(f);                             // exact: the values are the type's own
 }
 template <class E>
@@ -72,35 +71,43 @@ __global__ __launch_bounds__(kBlock) void combine_kernel(const CombineArgs a, in
     store_piece(static_cast<E *>(a.out) + t * a.H + col, n, acc);
 }
 
-// A wave per (token, choice): d_y[row] = w d_out[t] and d_w = <d_out[t],
-// y[row]>, the token's d_out row read by the neighbouring waves of the block
-// from the cache.  The blocks after those zero the rows no token owns.
-template <class E>
+// W lanes per (token, choice): d_y[row] = w d_out[t] and d_w = <d_out[t],
+// y[row]>, the token's d_out row read by its other choices from the cache.
+// The blocks after those zero the rows no token owns.  HBM-bound: every row of
+// y is read and every row of d_y written once.
+//
+// The lanes and the pieces in flight follow the row's length (8192 tokens of
+// 8 x 200 bf16: 25 us on whole waves).
+template <class E, int W, int U>
 __global__ __launch_bounds__(kBlock) void combine_backward_kernel(const CombineArgs a, int64_t pair_blocks) {
     constexpr int kV = Elem<E>::kVec;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     E *d_y = static_cast<E *>(a.d_y);
     if ((int64_t)blockIdx.x < pair_blocks) {
-        const int64_t p = (int64_t)blockIdx.x * (kBlock / 64) + wave;
-        if (p >= a.T * a.k) return;
-        const int64_t t = p / a.k;
-        const int64_t row = a.pair_row[p];
-        const float w = a.w[p];
-        const bool real = row >= 0 && row < a.rows;
+        const int64_t p = ((int64_t)blockIdx.x * kBlock + threadIdx.x) / W;
+        const bool live = p < a.T * a.k;
+        const int64_t row = live ? a.pair_row[p] : -1;
         float dot = 0.0f;
-        if (real) {
-            const E *d = static_cast<const E *>(a.d_out) + t * a.H;
+        if (row >= 0 && row < a.rows) {
+            const float w = a.w[p];
+            const E *d = static_cast<const E *>(a.d_out) + p / a.k * a.H;
             const E *y = static_cast<const E *>(a.y) + row * a.H;
-            int64_t col = lane * kV;
-            for (; col + 3 * 64 * kV + kV <= a.H; col += 4 * 64 * kV) {
-                v4u rg[4], rf[4];
+            E *dst = d_y + row * a.H;
+            for (int64_t col = (lane & (W - 1)) * kV; col < a.H; col += U * W * kV) {
+                v4u rg[U], rf[U];
+                int n[U];
 #pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    rf[u] = load16(y + col + u * 64 * kV);
-                    rg[u] = load16(d + col + u * 64 * kV);
+                for (int u = 0; u < U; ++u) {
+                    const int64_t at = col + u * W * kV;
+                    n[u] = (int)(a.H - at < kV ? a.H - at : kV);
+                    if (n[u] > 0) {
+                        rf[u] = load_piece(y + at, n[u]);
+                        rg[u] = load_piece(d + at, n[u]);
+                    }
                 }
 #pragma unroll
-                for (int u = 0; u < 4; ++u) {
+                for (int u = 0; u < U; ++u) {
+                    if (n[u] <= 0) break;
                     float g[kV], f[kV];
                     Elem<E>::unpack(rg[u], g);
                     Elem<E>::unpack(rf[u], f);
@@ -109,24 +116,12 @@ __global__ __launch_bounds__(kBlock) void combine_backward_kernel(const CombineA
                         dot = __builtin_fmaf(g[e], f[e], dot);
                         g[e] *= w;
                     }
-                    store16(d_y + row * a.H + col + u * 64 * kV, Elem<E>::pack(g));
+                    store_piece(dst + col + u * W * kV, n[u], g);
                 }
-            }
-            for (; col < a.H; col += 64 * kV) {
-                const int n = (int)(a.H - col < kV ? a.H - col : kV);
-                float g[kV], f[kV];
-                Elem<E>::unpack(load_piece(d + col, n), g);
-                Elem<E>::unpack(load_piece(y + col, n), f);
-#pragma unroll
-                for (int e = 0; e < kV; ++e) {
-                    dot = __builtin_fmaf(g[e], f[e], dot);
-                    g[e] *= w;
-                }
-                store_piece(d_y + row * a.H + col, n, g);
             }
         }
-        dot = group_reduce<64>(dot, OpAdd());
-        if (lane == 0) a.d_w[p] = dot;
+        dot = group_reduce<W>(dot, OpAdd());
+        if (live && (lane & (W - 1)) == 0) a.d_w[p] = dot;
         return;
     }
     const int64_t base = (((int64_t)blockIdx.x - pair_blocks) * (kBlock / 64) + wave) * kZeroRows;
@@ -156,11 +151,25 @@ hipError_t launch_combine(const CombineArgs &a, bool bf16, hipStream_t stream) {
     return hipGetLastError();
 }
 
-hipError_t launch_combine_backward(const CombineArgs &a, bool bf16, hipStream_t stream) {
-    const int64_t pair_blocks = ceil_div(a.T * a.k, kBlock / 64);
+template <class E, int W, int U>
+static void start_backward(const CombineArgs &a, hipStream_t stream) {
+    const int64_t pair_blocks = ceil_div(a.T * a.k, kBlock / W);
     const unsigned grid = (unsigned)(pair_blocks + ceil_div(a.rows, kBlock / 64 * kZeroRows));
-    if (bf16) combine_backward_kernel<uint16_t><<<grid, kBlock, 0, stream>>>(a, pair_blocks);
-    else combine_backward_kernel<float><<<grid, kBlock, 0, stream>>>(a, pair_blocks);
+    combine_backward_kernel<E, W, U><<<grid, kBlock, 0, stream>>>(a, pair_blocks);
+}
+template <class E>
+static void start_backward(const CombineArgs &a, hipStream_t stream) {
+    const int64_t pieces = ceil_div(a.H, Elem<E>::kVec);             // of a row
+    if (pieces <= 16) start_backward<E, 16, 1>(a, stream);
+    else if (pieces <= 32) start_backward<E, 32, 1>(a, stream);
+    else if (pieces <= 64) start_backward<E, 64, 1>(a, stream);
+    else if (pieces <= 128) start_backward<E, 64, 2>(a, stream);
+    else start_backward<E, 64, 4>(a, stream);
+}
+
+hipError_t launch_combine_backward(const CombineArgs &a, bool bf16, hipStream_t stream) {
+    if (bf16) start_backward<uint16_t>(a, stream);
+    else start_backward<float>(a, stream);
     return hipGetLastError();
 }
 

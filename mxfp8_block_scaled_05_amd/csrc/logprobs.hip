@@ -203,9 +203,11 @@ __device__ __forceinline__ void load_logits(const E *p, int64_t n, float *x) {
     constexpr int kV = Elem<E>::kVec;
     if (n >= kV) {
         Elem<E>::unpack(load16(p), x);
+    } else if (n > 0) {
+        load_head<kV>(p, (int)n, -__builtin_inff(), x);
     } else {
 #pragma unroll
-        for (int i = 0; i < kV; ++i) x[i] = i < n ? Elem<E>::get(p[i]) : -__builtin_inff();
+        for (int i = 0; i < kV; ++i) x[i] = -__builtin_inff();
     }
 }
 
@@ -386,15 +388,20 @@ __global__ __launch_bounds__(64) void logprobs_join_kernel(const LogprobsArgs a)
 // gradients of log-probability and entropy, log p = x / temp - m - log_sum.
 // One read and one write of the logits; in place is fine (a thread writes
 // what it alone has read).
-template <class E>
-__global__ __launch_bounds__(kBlock) void logprobs_backward_kernel(const LogprobsArgs a) {
-    constexpr int kV = Elem<E>::kVec;
+template <class E, int BLOCK>
+__global__ __launch_bounds__(BLOCK) void logprobs_backward_kernel(const LogprobsArgs a) {
+    constexpr int kV = Elem<E>::kVec, kStep = BLOCK * kV;
     const int64_t t = (int64_t)blockIdx.x / a.slices;
     const int slice = (int)((int64_t)blockIdx.x - t * a.slices);
     const int64_t lo = slice * a.slice;
     const int64_t hi = lo + a.slice < a.V ? lo + a.slice : a.V;
     const E *row = static_cast<const E *>(a.x) + t * a.ld;
     E *out = static_cast<E *>(a.dx) + t * a.ld_out;
+    const int64_t col = lo + threadIdx.x * kV;
+    v4u r[kUnroll];                                  // a thread's whole share, before anything is written
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u)
+        if (hi - col - u * kStep >= kV) r[u] = load16(row + col + u * kStep);
     const int64_t target = a.targets[t];
     const bool real = target >= 0 && target < a.V;
     const float g = real && a.d_logprobs ? a.d_logprobs[t] : 0.0f;
@@ -403,29 +410,27 @@ __global__ __launch_bounds__(kBlock) void logprobs_backward_kernel(const Logprob
     const float m = a.stats[2 * t], log_sum = a.stats[2 * t + 1];
     const float inv = a.inv, inv_low = a.inv_low;                            // 1 / temp = inv + inv_low
     const float c0 = -(g + h * H) * inv, c1 = -h * inv, at_target = g * inv;
-    for (int64_t col = lo + threadIdx.x * kV; col < hi; col += kBlock * kV) {
-        float x[kV];
-        const int64_t n = hi - col;
-        if (n >= kV) {
-            Elem<E>::unpack(load16(row + col), x);
-        } else {
 #pragma unroll
-            for (int i = 0; i < kV; ++i) x[i] = i < n ? Elem<E>::get(row[col + i]) : 0.0f;
-        }
+    for (int u = 0; u < kUnroll; ++u) {
+        const int64_t at = col + u * kStep, n = hi - at;
+        if (n <= 0) break;
+        float x[kV];
+        if (n >= kV) Elem<E>::unpack(r[u], x);
+        else load_head<kV>(row + at, (int)n, 0.0f, x);
 #pragma unroll
         for (int i = 0; i < kV; ++i) {
             const float logp = __builtin_fmaxf(__builtin_fmaf(x[i], inv, __builtin_fmaf(x[i], inv_low, -m)) - log_sum, -1000.0f);
             const float p = __builtin_amdgcn_exp2f(logp * kLog2E);
             float d = p * __builtin_fmaf(c1, logp, c0);
-            if (col + i == target) d += at_target;
+            if (at + i == target) d += at_target;
             x[i] = d;
         }
         if (n >= kV) {
-            store16(out + col, Elem<E>::pack(x));
+            store16(out + at, Elem<E>::pack(x));
         } else {
 #pragma unroll
             for (int i = 0; i < kV; ++i)
-                if (i < n) out[col + i] = Elem<E>::put(x[i]);
+                if (i < n) out[at + i] = Elem<E>::put(x[i]);
         }
     }
 }
@@ -488,11 +493,20 @@ hipError_t launch_logprobs_backward(LogprobsArgs a, bool bf16, hipStream_t strea
     a.inv_temperature = 1.0 / a.temperature;
     a.inv = (float)a.inv_temperature;
     a.inv_low = (float)(a.inv_temperature - a.inv);
-    a.slice = 4 * kBlock * (bf16 ? 8 : 4);
-    a.slices = (int)ceil_div(a.V, a.slice);
+    // blocks of kUnroll 16-byte pieces a thread at most, a row's blocks of about the same length
+    const int vec = bf16 ? 8 : 4;
+    const bool narrow = a.V <= kUnroll * vec * 64;
+    const int64_t most = kUnroll * vec * (narrow ? 64 : kBlock);
+    a.slices = (int)ceil_div(a.V, most);
+    a.slice = ceil_div(ceil_div(a.V, a.slices), vec) * vec;
     const unsigned grid = (unsigned)(a.T * a.slices);
-    if (bf16) logprobs_backward_kernel<uint16_t><<<grid, kBlock, 0, stream>>>(a);
-    else logprobs_backward_kernel<float><<<grid, kBlock, 0, stream>>>(a);
+    if (narrow) {
+        if (bf16) logprobs_backward_kernel<uint16_t, 64><<<grid, 64, 0, stream>>>(a);
+        else logprobs_backward_kernel<float, 64><<<grid, 64, 0, stream>>>(a);
+    } else {
+        if (bf16) logprobs_backward_kernel<uint16_t, kBlock><<<grid, kBlock, 0, stream>>>(a);
+        else logprobs_backward_kernel<float, kBlock><<<grid, kBlock, 0, stream>>>(a);
+    }
     return hipGetLastError();
 }
 

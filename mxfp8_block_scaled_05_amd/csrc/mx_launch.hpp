@@ -203,7 +203,7 @@ struct RouteTables {
     int64_t chunk;
     int chunks, id_bits, width;
 };
-int64_t route_tables_chunk(int64_t pairs);
+int64_t route_tables_workspace_bytes(int64_t pairs, int64_t E);
 hipError_t launch_route_tables(RouteTables a, hipStream_t stream);
 
 // Expert rows back to tokens (combine.hip)

@@ -119,6 +119,17 @@ struct Elem<uint16_t> {
     }
 };
 
+// The first `count` of N values at p, the rest `pad`.  Loads without a branch:
+// one each element would cost a round trip each.  p[0] is read whatever count is.
+template <int N, class E>
+__device__ __forceinline__ void load_head(const E *p, int count, float pad, float *x) {
+    E r[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) r[i] = p[i < count ? i : 0];
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = i < count ? Elem<E>::get(r[i]) : pad;
+}
+
 // ---------------------------------------------------------------- keys
 
 // Unsigned integers in the order of the floats (-Inf lowest; a NaN above

@@ -21,12 +21,7 @@ __device__ __forceinline__ void load_values(const E *p, int count, float pad, fl
             return;
         }
     }
-    // loads without a branch (one each element costs a round trip each)
-    E r[NV];
-#pragma unroll
-    for (int i = 0; i < NV; ++i) r[i] = p[i < count ? i : 0];
-#pragma unroll
-    for (int i = 0; i < NV; ++i) x[i] = i < count ? Elem<E>::get(r[i]) : pad;
+    load_head<NV>(p, count, pad, x);
 }
 
 // Reduction over aligned groups of 2^shift lanes, shift known at run time

@@ -8,6 +8,7 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kWavesT = kThreads / 64;
+constexpr int kAlone = 8;          // most chunks without a counting pass of their own; ids of a thread in flight
 
 __device__ __forceinline__ bool real_expert(int id, int E) { return (unsigned)id < (unsigned)E; }
 
@@ -30,10 +31,12 @@ __global__ __launch_bounds__(kThreads) void route_count_kernel(const RouteTables
 // that expert in earlier chunks, earlier waves of the chunk, and earlier in
 // the wave, so rows come in (expert, pair) order whatever runs first.  The
 // rank inside a wave is the count of lower lanes with the same expert, found
-// with one ballot per bit of the id.  One chunk needs no counts from before.
+// with one ballot per bit of the id.  Without a table of the chunks' counts
+// (hist null: few chunks) a block counts all pairs itself.
 __global__ __launch_bounds__(kThreads) void route_place_kernel(const RouteTables a) {
     __shared__ int start[kTablesMaxExperts + 1];     // padded group starts
     __shared__ int total[kTablesMaxExperts];
+    __shared__ int ahead[kTablesMaxExperts];         // hist null: pairs in earlier chunks
     __shared__ int at[kWavesT][kTablesMaxExperts];   // next row of (wave, expert)
     __shared__ int sums[kWavesT];
     __shared__ int2 joined[kThreads];
@@ -41,6 +44,8 @@ __global__ __launch_bounds__(kThreads) void route_place_kernel(const RouteTables
     for (int e = tid; e < a.E; e += kThreads)
 #pragma unroll
         for (int w = 0; w < kWavesT; ++w) at[w][e] = 0;
+    if (!a.hist)
+        for (int e = tid; e < a.E; e += kThreads) ahead[e] = total[e] = 0;    // pairs of the chunks before, after
     __syncthreads();
 
     const int64_t lo = (int64_t)blockIdx.x * a.chunk;
@@ -52,6 +57,19 @@ __global__ __launch_bounds__(kThreads) void route_place_kernel(const RouteTables
         const int id = a.ids[p];
         if (real_expert(id, a.E)) atomicAdd(&at[wave][id], 1);
     }
+    if (!a.hist) {
+        for (int64_t p0 = 0; p0 < a.pairs; p0 += kAlone * kThreads) {
+            int id[kAlone];
+#pragma unroll
+            for (int u = 0; u < kAlone; ++u) {
+                const int64_t p = p0 + u * kThreads + tid;
+                id[u] = p < a.pairs && (p < lo || p >= hi) ? a.ids[p] : -1;
+            }
+#pragma unroll
+            for (int u = 0; u < kAlone; ++u)
+                if (real_expert(id[u], a.E)) atomicAdd(p0 + u * kThreads + tid < lo ? &ahead[id[u]] : &total[id[u]], 1);
+        }
+    }
     __syncthreads();
 
     // pairs of every expert in all chunks and in the chunks before this one:
@@ -60,8 +78,12 @@ __global__ __launch_bounds__(kThreads) void route_place_kernel(const RouteTables
         const int e = e0 + (tid & (a.width - 1)), part = tid / a.width;
         int all = 0, before = 0;
         if (e < a.E) {
-            if (a.chunks == 1) {
-                for (int w = part; w < kWavesT; w += kThreads / a.width) all += at[w][e];
+            if (!a.hist) {
+                if (part == 0) {
+                    for (int w = 0; w < kWavesT; ++w) all += at[w][e];
+                    before = ahead[e];
+                    all += before + total[e];
+                }
             } else {
 #pragma unroll 8
                 for (int c = part; c < a.chunks; c += kThreads / a.width) {
@@ -144,10 +166,15 @@ __global__ __launch_bounds__(kThreads) void route_place_kernel(const RouteTables
 
 // Chunks of pairs, one block each: one chunk while a block can place them in
 // a few steps, then at most kTablesMaxChunks.
-int64_t route_tables_chunk(int64_t pairs) {
+static int64_t route_tables_chunk(int64_t pairs) {
     int64_t chunk = 2 * kThreads;
     if (ceil_div(pairs, chunk) > kTablesMaxChunks) chunk = ceil_div(ceil_div(pairs, kTablesMaxChunks), kThreads) * kThreads;
     return chunk;
+}
+
+int64_t route_tables_workspace_bytes(int64_t pairs, int64_t E) {
+    const int64_t chunks = ceil_div(pairs, route_tables_chunk(pairs));
+    return chunks > kAlone ? chunks * E * 4 : 0;
 }
 
 hipError_t launch_route_tables(RouteTables a, hipStream_t stream) {
@@ -157,7 +184,8 @@ hipError_t launch_route_tables(RouteTables a, hipStream_t stream) {
     while ((1 << a.id_bits) < a.E) ++a.id_bits;
     a.width = 64;
     while (a.width < a.E && a.width < kThreads) a.width <<= 1;
-    if (a.chunks > 1) route_count_kernel<<<(unsigned)a.chunks, kThreads, 0, stream>>>(a);
+    if (a.chunks <= kAlone) a.hist = nullptr;
+    if (a.hist) route_count_kernel<<<(unsigned)a.chunks, kThreads, 0, stream>>>(a);
     route_place_kernel<<<(unsigned)a.chunks, kThreads, 0, stream>>>(a);
     return hipGetLastError();
 }
