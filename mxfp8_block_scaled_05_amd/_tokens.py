@@ -6,7 +6,7 @@ import ctypes
 
 import torch
 
-from . import MXFP8_BF16, MXFP8_F32, lib
+from . import MXFP8_BF16, MXFP8_F32, _need, lib
 
 _ready = None
 
@@ -39,10 +39,25 @@ def tokens_lib():
 
 _CODES = {torch.float32: MXFP8_F32, torch.bfloat16: MXFP8_BF16}
 
+# The checks below look at the usual tensor first and leave what is not one to
+# the slower code that names the fault: a small call spends more time in
+# Python than on the device.
 
-def need_rows(t: torch.Tensor, name: str):
+
+def need(t, dtype, name: str) -> int:
+    """The address of a contiguous device tensor of that dtype."""
+    if t.__class__ is not torch.Tensor or t.dtype is not dtype or not t.is_cuda or not t.is_contiguous():
+        _need(t, dtype, name)
+    return t.data_ptr()
+
+
+def need_rows(t, name: str):
     """(dtype code, row stride) of a 2-D fp32 or bf16 device tensor whose rows
     are contiguous; the rows themselves may lie further apart."""
+    if t.__class__ is torch.Tensor and t.is_cuda and t.dim() == 2 and t.is_contiguous():
+        code = _CODES.get(t.dtype)
+        if code is not None:
+            return code, t.shape[1] or 1
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch.Tensor" % name)
     code = _CODES.get(t.dtype)
@@ -61,8 +76,13 @@ def need_rows(t: torch.Tensor, name: str):
     return code, ld
 
 
-def same_device(first: torch.Tensor, *others):
+def same_device(first, *others) -> int:
+    """The index of the one device of the tensors (None: left out)."""
     d = first.get_device()
     for t in others:
         if t is not None and t.get_device() != d:
             raise ValueError("all tensors must be on one device, got %s and %s" % (first.device, t.device))
+    return d
+
+
+stream_of = torch._C._cuda_getCurrentRawStream      # device index -> handle of its current stream

@@ -93,7 +93,28 @@ __global__ __launch_bounds__(kBlock) void combine_backward_kernel(const CombineA
             const E *d = static_cast<const E *>(a.d_out) + p / a.k * a.H;
             const E *y = static_cast<const E *>(a.y) + row * a.H;
             E *dst = d_y + row * a.H;
-            for (int64_t col = (lane & (W - 1)) * kV; col < a.H; col += U * W * kV) {
+            int64_t col = (lane & (W - 1)) * kV, base = 0;
+            for (; base + U * W * kV <= a.H; base += U * W * kV, col += U * W * kV) {
+                v4u rg[U], rf[U];
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    rf[u] = load16(y + col + u * W * kV);
+                    rg[u] = load16(d + col + u * W * kV);
+                }
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    float g[kV], f[kV];
+                    Elem<E>::unpack(rg[u], g);
+                    Elem<E>::unpack(rf[u], f);
+#pragma unroll
+                    for (int e = 0; e < kV; ++e) {
+                        dot = __builtin_fmaf(g[e], f[e], dot);
+                        g[e] *= w;
+                    }
+                    store16(dst + col + u * W * kV, Elem<E>::pack(g));
+                }
+            }
+            if (col < a.H) {                             // the rest, in flight together as well
                 v4u rg[U], rf[U];
                 int n[U];
 #pragma unroll

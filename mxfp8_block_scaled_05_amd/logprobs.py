@@ -10,8 +10,8 @@ from dataclasses import dataclass
 
 import torch
 
-from . import _check, _need, _ptr, _stream
-from ._tokens import need_rows, same_device, tokens_lib
+from . import _check
+from ._tokens import need, need_rows, same_device, stream_of, tokens_lib
 
 
 @dataclass
@@ -25,12 +25,11 @@ class TokenLogprobs:
 
 def _logits_targets(logits, targets):
     code, ld = need_rows(logits, "logits")
-    _need(targets, torch.int64, "targets")
+    ids = need(targets, torch.int64, "targets")
     T, V = logits.shape
     if targets.numel() != T:
         raise ValueError("targets must have T = %d entries" % T)
-    same_device(logits, targets)
-    return code, ld, T, V
+    return code, ld, T, V, ids, same_device(logits, targets)
 
 
 def token_logprobs(logits: torch.Tensor, targets: torch.Tensor, *, temperature: float = 1.0,
@@ -39,7 +38,7 @@ def token_logprobs(logits: torch.Tensor, targets: torch.Tensor, *, temperature: 
     softmax(logits / temperature), the entropy, and the ``top_n`` (at most 64)
     likeliest columns with theirs, from one pass over logits (fp32 or bf16
     [T, V], rows contiguous, any row stride) (mxfp8_token_logprobs)."""
-    code, ld, T, V = _logits_targets(logits, targets)
+    code, ld, T, V, tg, dev = _logits_targets(logits, targets)
     L = tokens_lib()
     logprobs = logits.new_empty(T, dtype=torch.float32)
     entropy = torch.empty_like(logprobs)
@@ -48,12 +47,12 @@ def token_logprobs(logits: torch.Tensor, targets: torch.Tensor, *, temperature: 
     if top_n:
         top = logprobs.new_empty((T, top_n))
         ids = targets.new_empty((T, top_n))
-    need = int(L.mxfp8_token_logprobs_workspace_bytes(T, V, top_n))
-    ws = logits.new_empty(need, dtype=torch.uint8) if need else None
-    _check(L.mxfp8_token_logprobs(_ptr(logits), code, ld, T, V, _ptr(targets), temperature, top_n, _ptr(logprobs),
-                                  _ptr(entropy), _ptr(stats), _ptr(top) if top_n else None,
-                                  _ptr(ids) if top_n else None, _ptr(ws) if need else None, need, _stream(logits.device)),
-           "mxfp8_token_logprobs")
+    need_ws = L.mxfp8_token_logprobs_workspace_bytes(T, V, top_n)
+    ws = logits.new_empty(need_ws, dtype=torch.uint8) if need_ws else None
+    _check(L.mxfp8_token_logprobs(logits.data_ptr(), code, ld, T, V, tg, temperature, top_n, logprobs.data_ptr(),
+                                  entropy.data_ptr(), stats.data_ptr(), top.data_ptr() if top_n else None,
+                                  ids.data_ptr() if top_n else None, ws.data_ptr() if need_ws else None, need_ws,
+                                  stream_of(dev)), "mxfp8_token_logprobs")
     return TokenLogprobs(logprobs, entropy, stats, top, ids)
 
 
@@ -64,19 +63,19 @@ def token_logprobs_backward(logits: torch.Tensor, targets: torch.Tensor, stats: 
     """Gradient of token_logprobs' logprobs and entropy with respect to the
     logits, in their dtype (mxfp8_token_logprobs_backward).  Either gradient
     may be None.  ``out`` may be the logits themselves (in place)."""
-    code, ld, T, V = _logits_targets(logits, targets)
+    code, ld, T, V, tg, dev = _logits_targets(logits, targets)
     if d_logprobs is None and d_entropy is None:
         raise ValueError("give d_logprobs, d_entropy or both")
     if d_entropy is not None and entropy is None:
         raise ValueError("d_entropy needs entropy")
-    _need(stats, torch.float32, "stats")
+    st = need(stats, torch.float32, "stats")
     if tuple(stats.shape) != (T, 2):
         raise ValueError("stats must be [T, 2]")
+    rows = []
     for t, name in ((entropy, "entropy"), (d_logprobs, "d_logprobs"), (d_entropy, "d_entropy")):
-        if t is not None:
-            _need(t, torch.float32, name)
-            if t.numel() != T:
-                raise ValueError("%s must have T = %d entries" % (name, T))
+        rows.append(None if t is None else need(t, torch.float32, name))
+        if t is not None and t.numel() != T:
+            raise ValueError("%s must have T = %d entries" % (name, T))
     same_device(logits, stats, entropy, d_logprobs, d_entropy)
     if out is None:
         out = logits.new_empty((T, V))
@@ -86,8 +85,7 @@ def token_logprobs_backward(logits: torch.Tensor, targets: torch.Tensor, stats: 
         if out_code != code or tuple(out.shape) != (T, V):
             raise ValueError("out must be [T, V] in the logits' dtype")
         same_device(logits, out)
-    _check(tokens_lib().mxfp8_token_logprobs_backward(
-        _ptr(logits), code, ld, T, V, _ptr(targets), _ptr(stats), _ptr(entropy) if entropy is not None else None,
-        _ptr(d_logprobs) if d_logprobs is not None else None, _ptr(d_entropy) if d_entropy is not None else None,
-        temperature, _ptr(out), ld_out, _stream(logits.device)), "mxfp8_token_logprobs_backward")
+    _check(tokens_lib().mxfp8_token_logprobs_backward(logits.data_ptr(), code, ld, T, V, tg, st, *rows, temperature,
+                                                      out.data_ptr(), ld_out, stream_of(dev)),
+           "mxfp8_token_logprobs_backward")
     return out

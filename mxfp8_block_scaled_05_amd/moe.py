@@ -13,8 +13,8 @@ from dataclasses import dataclass
 
 import torch
 
-from . import _check, _need, _ptr, _stream
-from ._tokens import need_rows, same_device, tokens_lib
+from . import _check
+from ._tokens import need, need_rows, same_device, stream_of, tokens_lib
 
 _SCORES = {"softmax": 0, "sigmoid": 1}
 
@@ -41,17 +41,18 @@ def route(logits: torch.Tensor, k: int, *, score: str = "softmax", bias: torch.T
     ``renormalize``, times ``scale``)."""
     code, ld = need_rows(logits, "logits")
     T, E = logits.shape
+    b = None
     if bias is not None:
-        _need(bias, torch.float32, "bias")
+        b = need(bias, torch.float32, "bias")
         if bias.numel() != E:
             raise ValueError("bias must have E = %d entries" % E)
-        same_device(logits, bias)
+    dev = same_device(logits, bias)
     sc = _score_code(score)
     ids = logits.new_empty((T, k), dtype=torch.int32)
     weights = logits.new_empty((T, k), dtype=torch.float32)
-    _check(tokens_lib().mxfp8_route(_ptr(logits), code, ld, T, E, k, sc, _ptr(bias) if bias is not None else None,
-                                    groups, groups_kept, group_top, renormalize, scale, _ptr(ids), _ptr(weights),
-                                    _stream(logits.device)), "mxfp8_route")
+    _check(tokens_lib().mxfp8_route(logits.data_ptr(), code, ld, T, E, k, sc, b, groups, groups_kept, group_top,
+                                    renormalize, scale, ids.data_ptr(), weights.data_ptr(), stream_of(dev)),
+           "mxfp8_route")
     return ids, weights
 
 
@@ -61,16 +62,14 @@ def route_backward(logits: torch.Tensor, ids: torch.Tensor, d_weights: torch.Ten
     logits' dtype (mxfp8_route_backward); arguments as route was given them."""
     code, ld = need_rows(logits, "logits")
     T, E = logits.shape
-    _need(ids, torch.int32, "ids")
-    _need(d_weights, torch.float32, "d_weights")
+    i, d = need(ids, torch.int32, "ids"), need(d_weights, torch.float32, "d_weights")
     if ids.dim() != 2 or ids.shape[0] != T or d_weights.shape != ids.shape:
         raise ValueError("ids and d_weights must both be [T = %d, k]" % T)
-    same_device(logits, ids, d_weights)
+    dev = same_device(logits, ids, d_weights)
     sc = _score_code(score)
     out = logits.new_empty((T, E))
-    _check(tokens_lib().mxfp8_route_backward(_ptr(logits), code, ld, T, E, ids.shape[1], sc, _ptr(ids),
-                                             _ptr(d_weights), renormalize, scale, _ptr(out),
-                                             _stream(logits.device)), "mxfp8_route_backward")
+    _check(tokens_lib().mxfp8_route_backward(logits.data_ptr(), code, ld, T, E, ids.shape[1], sc, i, d, renormalize,
+                                             scale, out.data_ptr(), stream_of(dev)), "mxfp8_route_backward")
     return out
 
 
@@ -93,15 +92,15 @@ def route_tables(ids: torch.Tensor, experts: int, pad: int = 32, rows: int | Non
     """Expert ids int32 [T, k] -> RouteTables: pairs sorted by (expert, token),
     groups padded to ``pad`` rows.  ``rows`` (default: route_rows, the most
     they can take) sizes row_token.  An id outside [0, experts) gets no row."""
-    _need(ids, torch.int32, "ids")
+    i = need(ids, torch.int32, "ids")
     if ids.dim() != 2:
         raise ValueError("ids must be [T, k]")
     T, k = ids.shape
     L = tokens_lib()
     if rows is None:
         rows = int(L.mxfp8_route_rows(T * k, experts, pad))
-    dev = ids.device
     if T == 0:
+        dev = ids.device
         return RouteTables(torch.zeros(experts + 1, dtype=torch.int32, device=dev),
                            torch.zeros(experts, dtype=torch.int32, device=dev),
                            torch.full((rows,), -1, dtype=torch.int64, device=dev),
@@ -110,41 +109,40 @@ def route_tables(ids: torch.Tensor, experts: int, pad: int = 32, rows: int | Non
     counts = ids.new_empty(experts)
     row_token = ids.new_empty(rows, dtype=torch.int64)
     pair_row = torch.empty_like(ids)
-    need = int(L.mxfp8_route_tables_workspace_bytes(T, k, experts))
-    ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-    _check(L.mxfp8_route_tables(_ptr(ids), T, k, experts, pad, _ptr(offsets), _ptr(counts), _ptr(row_token), rows,
-                                _ptr(pair_row), _ptr(ws) if need else None, need, _stream(dev)),
-           "mxfp8_route_tables")
+    need_ws = L.mxfp8_route_tables_workspace_bytes(T, k, experts)
+    ws = ids.new_empty(need_ws // 4) if need_ws else None
+    _check(L.mxfp8_route_tables(i, T, k, experts, pad, offsets.data_ptr(), counts.data_ptr(), row_token.data_ptr(), rows,
+                                pair_row.data_ptr(), ws.data_ptr() if need_ws else None, need_ws,
+                                stream_of(ids.get_device())), "mxfp8_route_tables")
     return RouteTables(offsets, counts, row_token, pair_row, pad)
 
 
 def _combine_args(y, pair_row, weights):
-    _need(y, y.dtype if isinstance(y, torch.Tensor) else None, "y")
     code, _ = need_rows(y, "y")
-    _need(pair_row, torch.int32, "pair_row")
-    _need(weights, torch.float32, "weights")
+    if not y.is_contiguous():
+        raise ValueError("y must be contiguous")
+    p, w = need(pair_row, torch.int32, "pair_row"), need(weights, torch.float32, "weights")
     if pair_row.dim() != 2 or weights.shape != pair_row.shape:
         raise ValueError("pair_row and weights must both be [T, k]")
-    same_device(y, pair_row, weights)
-    return code
+    return code, p, w
 
 
 def moe_combine(y: torch.Tensor, pair_row: torch.Tensor, weights: torch.Tensor,
                 out: torch.Tensor | None = None) -> torch.Tensor:
     """out[t] = sum_j weights[t, j] * y[pair_row[t, j]] in fp32, rounded once
     to y's dtype (mxfp8_moe_combine).  y fp32 or bf16 [rows, H]."""
-    code = _combine_args(y, pair_row, weights)
+    code, p, w = _combine_args(y, pair_row, weights)
     T, k = pair_row.shape
     rows, H = y.shape
     if out is None:
         out = y.new_empty((T, H))
     else:
-        _need(out, y.dtype, "out")
+        need(out, y.dtype, "out")
         if tuple(out.shape) != (T, H):
             raise ValueError("out must be [T, H]")
-        same_device(y, out)
-    _check(tokens_lib().mxfp8_moe_combine(_ptr(y), code, rows, H, _ptr(pair_row), _ptr(weights), T, k, _ptr(out),
-                                          _stream(y.device)), "mxfp8_moe_combine")
+    dev = same_device(y, pair_row, weights, out)
+    _check(tokens_lib().mxfp8_moe_combine(y.data_ptr(), code, rows, H, p, w, T, k, out.data_ptr(), stream_of(dev)),
+           "mxfp8_moe_combine")
     return out
 
 
@@ -152,17 +150,15 @@ def moe_combine_backward(d_out: torch.Tensor, y: torch.Tensor, pair_row: torch.T
                          row_token: torch.Tensor):
     """Gradients of moe_combine: (d_y [rows, H] in y's dtype, zeros in padding
     rows; d_weights fp32 [T, k]) (mxfp8_moe_combine_backward)."""
-    code = _combine_args(y, pair_row, weights)
+    code, p, w = _combine_args(y, pair_row, weights)
     T, k = pair_row.shape
     rows, H = y.shape
-    _need(d_out, y.dtype, "d_out")
-    _need(row_token, torch.int64, "row_token")
+    d, r = need(d_out, y.dtype, "d_out"), need(row_token, torch.int64, "row_token")
     if tuple(d_out.shape) != (T, H) or row_token.numel() != rows:
         raise ValueError("d_out must be [T = %d, H = %d] and row_token [%d]" % (T, H, rows))
-    same_device(y, d_out, row_token)
+    dev = same_device(y, pair_row, weights, d_out, row_token)
     d_y = torch.empty_like(y)
     d_w = torch.empty_like(weights)
-    _check(tokens_lib().mxfp8_moe_combine_backward(_ptr(d_out), _ptr(y), code, rows, H, _ptr(pair_row),
-                                                   _ptr(weights), _ptr(row_token), T, k, _ptr(d_y), _ptr(d_w),
-                                                   _stream(y.device)), "mxfp8_moe_combine_backward")
+    _check(tokens_lib().mxfp8_moe_combine_backward(d, y.data_ptr(), code, rows, H, p, w, r, T, k, d_y.data_ptr(),
+                                                   d_w.data_ptr(), stream_of(dev)), "mxfp8_moe_combine_backward")
     return d_y, d_w
