@@ -34,7 +34,12 @@ __device__ __forceinline__ void store_piece(E *p, int n, const float *f) {
 
 // out[t] = sum_j w[t][j] y[pair_row[t][j]], in fp32 and in the order of j,
 // rounded once.  HBM-bound: every chosen row is read once.  A thread holds
-// one 16-byte piece of one token.
+// one 16-byte piece of one token and asks for it in 8 of the token's rows
+// before it adds any: 8192 tokens of 8 x 2048 bf16 take 47.2 us with part of
+// y still in the last-level cache and 59.7 us (5.07 TB/s) from HBM; one row
+// after another took 65 us.  Its loads are the row pieces of neighbouring
+// threads, so any row length and alignment keeps the rate (1001 columns: 5.2
+// TB/s).
 template <class E>
 __global__ __launch_bounds__(kBlock) void combine_kernel(const CombineArgs a, int64_t pieces) {
     constexpr int kV = Elem<E>::kVec;
@@ -74,10 +79,14 @@ __global__ __launch_bounds__(kBlock) void combine_kernel(const CombineArgs a, in
 // W lanes per (token, choice): d_y[row] = w d_out[t] and d_w = <d_out[t],
 // y[row]>, the token's d_out row read by its other choices from the cache.
 // The blocks after those zero the rows no token owns.  HBM-bound: every row of
-// y is read and every row of d_y written once.
+// y is read and every row of d_y written once (4095 tokens of 8 x 2048 bf16:
+// 52.8 us, 61.6 us or 4.9 TB/s from HBM).
 //
-// The lanes and the pieces in flight follow the row's length (8192 tokens of
-// 8 x 200 bf16: 25 us on whole waves).
+// The lanes and the pieces in flight follow the row's length: 8192 tokens of
+// 8 x 200 bf16 take 15.6 us, 25.2 us on whole waves; 8192 x 1 x 64 fp32 3.7
+// us, 7.1 us.  Whole strides go without guards (60.4 us with them).  Rows of an odd
+// number of bf16 lose a third (8 x 1001: 3.3 TB/s): cutting the pieces at
+// multiples of 16 bytes of d_y did not help (109 against 86 us).
 template <class E, int W, int U>
 __global__ __launch_bounds__(kBlock) void combine_backward_kernel(const CombineArgs a, int64_t pair_blocks) {
     constexpr int kV = Elem<E>::kVec;

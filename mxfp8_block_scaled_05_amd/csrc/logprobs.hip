@@ -255,12 +255,16 @@ __device__ __forceinline__ uint64_t *part_keys(const LogprobsArgs &a) {
 }
 
 // One pass over a slice of a row: running maximum, sum and weighted sum per
-// lane, joined over the block.
+// lane, joined over the block.  2048 rows of 131072 bf16 take 91 us, 5.9 TB/s
+// (a large copy moves 5.3): HBM and the vector ALU (9.2 instructions a logit, busy
+// for 94% of the time) are both at their limits; one row of 131072 5.1 us.
 //
 // The best n: the pass keeps each thread's largest logit only.  n threads'
 // largest reach the n-th largest of them, so no logit below that bar is among
 // the best, and few threads hold one above it: their logits alone are looked
 // at again (n / BLOCK of the row), those above the bar gathered and ranked.
+// 2048 rows of 131072 bf16 with n = 5: 107 us (a list kept sorted during the
+// pass: 182); one row with n = 20: 12.6 us with the join (22).
 template <class E, bool TOP, int BLOCK>
 __global__ __launch_bounds__(BLOCK) void logprobs_kernel(const LogprobsArgs a) {
     constexpr int kV = Elem<E>::kVec, kWaves = BLOCK / 64;
@@ -387,7 +391,9 @@ __global__ __launch_bounds__(64) void logprobs_join_kernel(const LogprobsArgs a)
 // d logits = (g (1[target] - p) - h p (log p + H)) / temp with g, h the
 // gradients of log-probability and entropy, log p = x / temp - m - log_sum.
 // One read and one write of the logits; in place is fine (a thread writes
-// what it alone has read).
+// what it alone has read).  2048 rows of 131072 bf16 take 187 us, 5.75 TB/s,
+// more than a large copy's 5.3.  A row of 9000 in two blocks of equal length
+// 53 us, cut at 8192 72 us (8000 rows).
 template <class E, int BLOCK>
 __global__ __launch_bounds__(BLOCK) void logprobs_backward_kernel(const LogprobsArgs a) {
     constexpr int kV = Elem<E>::kVec, kStep = BLOCK * kV;
