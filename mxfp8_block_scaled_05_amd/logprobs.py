@@ -42,13 +42,13 @@ def token_logprobs(logits: torch.Tensor, targets: torch.Tensor, *, temperature: 
     L = tokens_lib()
     logprobs = logits.new_empty(T, dtype=torch.float32)
     entropy = torch.empty_like(logprobs)
-    stats = logprobs.new_empty((T, 2))
+    stats = logprobs.new_empty(T, 2)
     top = ids = None
     if top_n:
-        top = logprobs.new_empty((T, top_n))
-        ids = targets.new_empty((T, top_n))
+        top = logprobs.new_empty(T, top_n)
+        ids = targets.new_empty(T, top_n)
     need_ws = L.mxfp8_token_logprobs_workspace_bytes(T, V, top_n)
-    ws = logits.new_empty(need_ws, dtype=torch.uint8) if need_ws else None
+    ws = logprobs.new_empty(need_ws // 4) if need_ws else None
     _check(L.mxfp8_token_logprobs(logits.data_ptr(), code, ld, T, V, tg, temperature, top_n, logprobs.data_ptr(),
                                   entropy.data_ptr(), stats.data_ptr(), top.data_ptr() if top_n else None,
                                   ids.data_ptr() if top_n else None, ws.data_ptr() if need_ws else None, need_ws,
@@ -78,7 +78,7 @@ def token_logprobs_backward(logits: torch.Tensor, targets: torch.Tensor, stats: 
             raise ValueError("%s must have T = %d entries" % (name, T))
     same_device(logits, stats, entropy, d_logprobs, d_entropy)
     if out is None:
-        out = logits.new_empty((T, V))
+        out = logits.new_empty(T, V)
         ld_out = V
     else:
         out_code, ld_out = need_rows(out, "out")

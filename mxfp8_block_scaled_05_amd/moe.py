@@ -49,7 +49,7 @@ def route(logits: torch.Tensor, k: int, *, score: str = "softmax", bias: torch.T
     dev = same_device(logits, bias)
     sc = _score_code(score)
     ids = logits.new_empty((T, k), dtype=torch.int32)
-    weights = logits.new_empty((T, k), dtype=torch.float32)
+    weights = torch.empty_like(ids, dtype=torch.float32)
     _check(tokens_lib().mxfp8_route(logits.data_ptr(), code, ld, T, E, k, sc, b, groups, groups_kept, group_top,
                                     renormalize, scale, ids.data_ptr(), weights.data_ptr(), stream_of(dev)),
            "mxfp8_route")
@@ -67,7 +67,7 @@ def route_backward(logits: torch.Tensor, ids: torch.Tensor, d_weights: torch.Ten
         raise ValueError("ids and d_weights must both be [T = %d, k]" % T)
     dev = same_device(logits, ids, d_weights)
     sc = _score_code(score)
-    out = logits.new_empty((T, E))
+    out = logits.new_empty(T, E)
     _check(tokens_lib().mxfp8_route_backward(logits.data_ptr(), code, ld, T, E, ids.shape[1], sc, i, d, renormalize,
                                              scale, out.data_ptr(), stream_of(dev)), "mxfp8_route_backward")
     return out
@@ -135,7 +135,7 @@ def moe_combine(y: torch.Tensor, pair_row: torch.Tensor, weights: torch.Tensor,
     T, k = pair_row.shape
     rows, H = y.shape
     if out is None:
-        out = y.new_empty((T, H))
+        out = y.new_empty(T, H)
     else:
         need(out, y.dtype, "out")
         if tuple(out.shape) != (T, H):
