@@ -167,8 +167,8 @@ __device__ __forceinline__ Best best_of(const uint64_t *keys, int count, int n, 
     return b;
 }
 
-// Unsigned order of a logit among a row's best: a NaN above all.
-__device__ __forceinline__ uint32_t logit_order(float x) { return x != x ? 0xFFFFFFFFu : order_key(x); }
+// Unsigned order of a logit among a row's best: a NaN above all, -0 as 0.
+__device__ __forceinline__ uint32_t logit_order(float x) { return x != x ? 0xFFFFFFFFu : order_key(x + 0.0f); }
 __device__ __forceinline__ uint64_t logit_key(float x, int64_t col) {
     return ((uint64_t)logit_order(x) << 32) | (uint32_t)~(uint32_t)col;
 }
@@ -310,7 +310,7 @@ __global__ __launch_bounds__(BLOCK) void logprobs_kernel(const LogprobsArgs a) {
 
     v = join_lanes(v, c);
     if (lane == 0) parts[wave] = v;
-    const uint32_t mine = order_key(most);
+    const uint32_t mine = logit_order(most);
     if constexpr (TOP) largest[threadIdx.x] = mine;
     __syncthreads();
     if constexpr (TOP) {

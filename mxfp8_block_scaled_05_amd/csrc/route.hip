@@ -104,7 +104,7 @@ __device__ __forceinline__ Fp64Row fp64_row(const RouteArgs &a, const E *row, co
 }
 // the value that decides: the biased score, or the logit where that has the same order
 __device__ __forceinline__ double fp64_value(const RouteArgs &a, const Fp64Row &r, float x, int id) {
-    if (a.order_x) return x;
+    if (a.order_x) return x + 0.0f;                      // -0 as 0
     const double s = a.sigmoid ? 1.0 / (1.0 + exp(-(double)x)) : exp((double)x - r.top) / r.total;
     return a.bias ? s + (double)a.bias[id] : s;
 }
@@ -223,6 +223,10 @@ __global__ __launch_bounds__(kBlock, 4) void route_kernel(const RouteArgs a) {
     float v[NV], bias[NV];
     load_values<NV>(row + (ex.count ? ex.first : 0), ex.count, kNone, v);
     if (a.bias) load_values<NV>(a.bias + (ex.count ? ex.first : 0), ex.count, 0.0f, bias);
+    if (a.order_x) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) v[i] += 0.0f;       // -0 as 0: equal logits get equal keys (scores are never -0)
+    }
     float top = v[0];
 #pragma unroll
     for (int i = 1; i < NV; ++i) top = __builtin_fmaxf(top, v[i]);

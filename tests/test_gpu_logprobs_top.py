@@ -63,3 +63,13 @@ def test_nan_rows_give_columns(mx):
     for row in r.top_ids.tolist():
         assert len(set(row)) == 20 and min(row) >= 0 and max(row) < 5000
     assert torch.isnan(r.top_logprobs[1:]).all() and torch.isfinite(r.top_logprobs[0]).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("T,V", [(2, 9000), (300, 20000), (1100, 700)])
+def test_zeros_of_both_signs_are_equal(mx, T, V, dtype):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(V)
+    x = torch.where(torch.rand((T, V), generator=g, device="cuda") < 0.5, -0.0, 0.0).to(dtype)
+    x[: T // 2, ::3] = -2.0
+    _check(mx, x, 9, "zeros")

@@ -71,3 +71,16 @@ def test_close_groups(mx, E, groups, score, group_top):
         kw = dict(score=score, groups=groups, groups_kept=kept, group_top=group_top)
         _check(mx, x, k, **kw)
         _check(mx, x, k, bias=torch.full((E,), 0.03, device="cuda"), **kw)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_zeros_of_both_signs_are_equal(mx, dtype):
+    print("zeros", dtype, flush=True)
+    rng = np.random.default_rng(8)
+    x = np.where(rng.random((40, 96)) < 0.5, -0.0, 0.0).astype(np.float32)
+    x[:20, ::5] = -1.0
+    x = torch.from_numpy(x).cuda().to(dtype)
+    zero = torch.zeros(96, device="cuda")
+    for kw in ({}, dict(score="sigmoid"), dict(groups=8, groups_kept=2), dict(groups=8, groups_kept=2, group_top=2),
+               dict(bias=zero), dict(score="sigmoid", bias=-zero)):
+        _check(mx, x, 7, **kw)
