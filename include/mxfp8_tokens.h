@@ -167,7 +167,8 @@ mxfp8_status mxfp8_token_logprobs(const void *logits, mxfp8_dtype dtype, int64_t
  *   d_logits[t][v] = (g (1[v = target] - p) - h p (log p + entropy)) /
  *   temperature, g = d_logprobs[t] (0 where the target is outside [0, V)),
  *   h = d_entropy[t]; a term whose gradient is NULL is left out (not both;
- *   entropy may be NULL with d_entropy).  Columns of -Inf get 0.
+ *   entropy may be NULL with d_entropy).  Columns of -Inf get 0 (the
+ *   target's g / temperature).
  *   stats and entropy as mxfp8_token_logprobs gave them for the same logits
  *   and temperature.  d_logits: rows ld_out >= V apart, in the logits' dtype;
  *   it may be the logits themselves (same pointer and ld).

@@ -8,9 +8,27 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kWavesT = kThreads / 64;
+constexpr int kCounts = 16;        // chunk counts of a thread in flight
 constexpr int kAlone = 8;          // most chunks without a counting pass of their own; ids of a thread in flight
 
 __device__ __forceinline__ bool real_expert(int id, int E) { return (unsigned)id < (unsigned)E; }
+
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int dpp_add(int v) {
+    return __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xF, false);
+}
+// Sum of the lanes up to and with one's own.  Inside a row of 16 and from row
+// to row the steps are lane shifts of the vector ALU; lanes that none reaches
+// add 0.
+__device__ __forceinline__ int wave_scan(int v) {
+    v += dpp_add<0x111, 0xF>(v);                    // row_shr:1
+    v += dpp_add<0x112, 0xF>(v);                    // row_shr:2
+    v += dpp_add<0x114, 0xF>(v);                    // row_shr:4
+    v += dpp_add<0x118, 0xF>(v);                    // row_shr:8
+    v += dpp_add<0x142, 0xA>(v);                    // row_bcast:15 into rows 1 and 3
+    v += dpp_add<0x143, 0xC>(v);                    // row_bcast:31 into rows 2 and 3
+    return v;
+}
 
 // counts of the experts in one chunk of pairs -> hist[chunk][E]
 __global__ __launch_bounds__(kThreads) void route_count_kernel(const RouteTables a) {
@@ -61,11 +79,12 @@ __global__ __launch_bounds__(kThreads) void route_place_kernel(const RouteTables
     const int64_t per = a.chunk / kWavesT;           // pairs of a wave, a multiple of 64
     const int64_t wlo = lo + wave * per;
     const int64_t whi = wlo + per < hi ? wlo + per : hi;
+#pragma unroll 4
     for (int64_t p = wlo + lane; p < whi; p += 64) {
         const int id = a.ids[p];
         if (real_expert(id, a.E)) atomicAdd(&at[wave][id], 1);
     }
-    if (!a.hist) {
+    if (!a.hist && a.chunks > 1) {
         for (int64_t p0 = 0; p0 < a.pairs; p0 += kAlone * kThreads) {
             int id[kAlone];
 #pragma unroll
@@ -93,11 +112,20 @@ __global__ __launch_bounds__(kThreads) void route_place_kernel(const RouteTables
                     all += before + total[e];
                 }
             } else {
-#pragma unroll 8
-                for (int c = part; c < a.chunks; c += kThreads / a.width) {
-                    const int n = a.hist[(int64_t)c * a.E + e];
-                    before += c < (int)blockIdx.x ? n : 0;
-                    all += n;
+                const int step = kThreads / a.width;
+                for (int c0 = part; c0 < a.chunks; c0 += kCounts * step) {
+                    int n[kCounts];
+#pragma unroll
+                    for (int u = 0; u < kCounts; ++u) {
+                        const int c = c0 + u * step;
+                        n[u] = a.hist[(int64_t)(c < a.chunks ? c : part) * a.E + e];
+                    }
+#pragma unroll
+                    for (int u = 0; u < kCounts; ++u) {
+                        const int c = c0 + u * step;
+                        before += c < (int)blockIdx.x ? n[u] : 0;
+                        all += c < a.chunks ? n[u] : 0;
+                    }
                 }
             }
         }
@@ -113,12 +141,7 @@ __global__ __launch_bounds__(kThreads) void route_place_kernel(const RouteTables
         }
         // exclusive scan of the padded totals over the experts
         const int padded = (all + a.pad - 1) / a.pad * a.pad;
-        int scan = padded;
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const int o = __shfl_up(scan, d, 64);
-            scan += lane >= d ? o : 0;
-        }
+        const int scan = wave_scan(padded);
         if (lane == 63) sums[wave] = scan;
         __syncthreads();
         int first = scan - padded + (e0 ? start[e0] : 0);
@@ -137,9 +160,11 @@ __global__ __launch_bounds__(kThreads) void route_place_kernel(const RouteTables
         __syncthreads();
     }
 
+    int ahead_id = wlo + lane < whi ? a.ids[wlo + lane] : -1;
     for (int64_t base = wlo; base < whi; base += 64) {
         const int64_t p = base + lane;
-        const int id = p < whi ? a.ids[p] : -1;
+        const int id = ahead_id;
+        ahead_id = p + 64 < whi ? a.ids[p + 64] : -1;
         const bool real = real_expert(id, a.E);
         uint64_t same = __ballot(real);
         for (int b = 0; b < a.id_bits; ++b) {
@@ -160,8 +185,9 @@ __global__ __launch_bounds__(kThreads) void route_place_kernel(const RouteTables
     }
 
     // padding rows, the rows past the last group, and the tables of the groups
-    for (int e = blockIdx.x * kWavesT + wave; e < a.E; e += gridDim.x * kWavesT)
-        for (int r = start[e] + total[e] + lane; r < start[e + 1]; r += 64) a.row_token[r] = -1;
+#pragma unroll 4
+    for (int e = blockIdx.x * (kThreads / 32) + tid / 32; e < a.E; e += gridDim.x * (kThreads / 32))
+        for (int r = start[e] + total[e] + (tid & 31); r < start[e + 1]; r += 32) a.row_token[r] = -1;
     for (int64_t r = start[a.E] + (int64_t)blockIdx.x * kThreads + tid; r < a.rows; r += (int64_t)gridDim.x * kThreads)
         a.row_token[r] = -1;
     if (blockIdx.x == 0) {
