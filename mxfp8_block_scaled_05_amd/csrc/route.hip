@@ -183,7 +183,7 @@ __device__ __forceinline__ void choose_fp64(const RouteArgs &a, const E *row, co
 // equals; w = s[ids], over their sum if renormalized, times scale.
 //
 // Bound by the vector ALU and by latency, not by memory: 16384 tokens of 256
-// sigmoid scores in 8 groups take 11.9 us (917 vector instructions a wave, the
+// sigmoid scores in 8 groups take 12.0 us (919 vector instructions a wave, the
 // ALU busy for 66% of it) where their bytes take 3.4 us; 128 softmax scores of one
 // token 3.2 us, a launch's own time.
 //

@@ -51,14 +51,15 @@ __global__ __launch_bounds__(kThreads) void route_count_kernel(const RouteTables
 // rank inside a wave is the count of lower lanes with the same expert, found
 // with one ballot per bit of the id.  Without a table of the chunks' counts
 // (hist null: few chunks) a block counts all pairs itself: 2048 pairs over 256
-// experts 7.7 us against 9.6 us with the counting launch before it, and that
+// experts 6.8 us against 9.6 us with the counting launch before it, and that
 // launch and its workspace cost the caller another 5 us.
 //
-// Latency-bound: a chain of loads, LDS counts and barriers of about 6 us for
-// any number of pairs that one chunk a unit holds (131072 pairs over 256
-// experts: 3.0 us of counting and 9.7 us; their bytes would take 0.4 us).  The chunk
-// counts are summed by several threads an expert with their loads in flight:
-// one thread an expert took 28.2 us.
+// Latency-bound: a chain of loads, LDS counts and barriers (256 pairs over 128
+// experts 5.7 us; 131072 pairs over 256 experts 3.0 us of counting and 9.1 us
+// here, where their bytes would take 0.4 us).  The chunk counts are summed by
+// several threads an expert with their loads in flight: one thread an expert
+// took 28.2 us.  Scans over lane shifts and padding rows by half waves save
+// 1.1 us of the chain.
 __global__ __launch_bounds__(kThreads) void route_place_kernel(const RouteTables a) {
     __shared__ int start[kTablesMaxExperts + 1];     // padded group starts
     __shared__ int total[kTablesMaxExperts];
