@@ -12,10 +12,10 @@ constexpr int kAhead = 8;          // rows of a token in flight
 constexpr int kZeroRows = 8;       // rows a wave looks over for padding
 
 // One 16-byte piece of a row: all of it, or its first n elements and zeros.
-template <class E>
+template <bool ONCE, class E>
 __device__ __forceinline__ v4u load_piece(const E *p, int n) {
     constexpr int kV = Elem<E>::kVec;
-    if (n >= kV) return load16(p);
+    if (n >= kV) return load16<ONCE>(p);
     float f[kV];
     load_head<kV>(p, n, 0.0f, f);
     return Elem<E>::pack(f);                             // exact: the values are the type's own
@@ -36,11 +36,13 @@ __device__ __forceinline__ void store_piece(E *p, int n, const float *f) {
 // rounded once.  HBM-bound: every chosen row is read once.  A thread holds
 // one 16-byte piece of one token and asks for it in 8 of the token's rows
 // before it adds any: 8192 tokens of 8 x 2048 bf16 take 47.2 us with part of
-// y still in the last-level cache and 59.7 us (5.07 TB/s) from HBM; one row
-// after another took 65 us.  Its loads are the row pieces of neighbouring
+// y still in the last-level cache; one row after another took 65 us.  ONCE (y
+// larger than that cache) reads past it: from HBM 52.5 us (5.8 TB/s) instead of
+// 59.4, after a copy that wrote y 151 us for both instead of 160; at 4095
+// tokens, where y fits, it would cost 26.8 us instead of 23.8.  Its loads are the row pieces of neighbouring
 // threads, so any row length and alignment keeps the rate (1001 columns: 5.2
 // TB/s).
-template <class E>
+template <class E, bool ONCE>
 __global__ __launch_bounds__(kBlock) void combine_kernel(const CombineArgs a, int64_t pieces) {
     constexpr int kV = Elem<E>::kVec;
     const int64_t i = (int64_t)blockIdx.x * kBlock + threadIdx.x;
@@ -63,7 +65,7 @@ __global__ __launch_bounds__(kBlock) void combine_kernel(const CombineArgs a, in
         }
 #pragma unroll
         for (int u = 0; u < kAhead; ++u)
-            if (row[u] >= 0 && row[u] < a.rows) r[u] = load_piece(y + row[u] * a.H, n);
+            if (row[u] >= 0 && row[u] < a.rows) r[u] = load_piece<ONCE>(y + row[u] * a.H, n);
 #pragma unroll
         for (int u = 0; u < kAhead; ++u)
             if (row[u] >= 0 && row[u] < a.rows) {
@@ -80,14 +82,17 @@ __global__ __launch_bounds__(kBlock) void combine_kernel(const CombineArgs a, in
 // y[row]>, the token's d_out row read by its other choices from the cache.
 // The blocks after those zero the rows no token owns.  HBM-bound: every row of
 // y is read and every row of d_y written once (4095 tokens of 8 x 2048 bf16:
-// 52.8 us, 61.6 us or 4.9 TB/s from HBM).
+// 52.8 us).  ONCE (both together larger than the last-level cache) keeps them
+// out of it: 55.2 us (5.5 TB/s) from HBM instead of 61.7, with the quantizer that
+// reads d_y next 182 us instead of 187 (8192 tokens); at 2000 tokens that pair
+// would take 52.1 us instead of 46.0.
 //
 // The lanes and the pieces in flight follow the row's length: 8192 tokens of
 // 8 x 200 bf16 take 15.6 us, 25.2 us on whole waves; 8192 x 1 x 64 fp32 3.7
 // us, 7.1 us.  Whole strides go without guards (60.4 us with them).  Rows of an odd
 // number of bf16 lose a third (8 x 1001: 3.3 TB/s): cutting the pieces at
 // multiples of 16 bytes of d_y did not help (109 against 86 us).
-template <class E, int W, int U>
+template <class E, int W, int U, bool ONCE>
 __global__ __launch_bounds__(kBlock) void combine_backward_kernel(const CombineArgs a, int64_t pair_blocks) {
     constexpr int kV = Elem<E>::kVec;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -107,7 +112,7 @@ __global__ __launch_bounds__(kBlock) void combine_backward_kernel(const CombineA
                 v4u rg[U], rf[U];
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
-                    rf[u] = load16(y + col + u * W * kV);
+                    rf[u] = load16<ONCE>(y + col + u * W * kV);
                     rg[u] = load16(d + col + u * W * kV);
                 }
 #pragma unroll
@@ -120,7 +125,7 @@ __global__ __launch_bounds__(kBlock) void combine_backward_kernel(const CombineA
                         dot = __builtin_fmaf(g[e], f[e], dot);
                         g[e] *= w;
                     }
-                    store16(dst + col + u * W * kV, Elem<E>::pack(g));
+                    store16<ONCE>(dst + col + u * W * kV, Elem<E>::pack(g));
                 }
             }
             if (col < a.H) {                             // the rest, in flight together as well
@@ -131,8 +136,8 @@ __global__ __launch_bounds__(kBlock) void combine_backward_kernel(const CombineA
                     const int64_t at = col + u * W * kV;
                     n[u] = (int)(a.H - at < kV ? a.H - at : kV);
                     if (n[u] > 0) {
-                        rf[u] = load_piece(y + at, n[u]);
-                        rg[u] = load_piece(d + at, n[u]);
+                        rf[u] = load_piece<ONCE>(y + at, n[u]);
+                        rg[u] = load_piece<false>(d + at, n[u]);
                     }
                 }
 #pragma unroll
@@ -176,8 +181,14 @@ __global__ __launch_bounds__(kBlock) void combine_backward_kernel(const CombineA
 hipError_t launch_combine(const CombineArgs &a, bool bf16, hipStream_t stream) {
     const int64_t pieces = ceil_div(a.H, bf16 ? 8 : 4);
     const unsigned grid = (unsigned)ceil_div(a.T * pieces, kBlock);
-    if (bf16) combine_kernel<uint16_t><<<grid, kBlock, 0, stream>>>(a, pieces);
-    else combine_kernel<float><<<grid, kBlock, 0, stream>>>(a, pieces);
+    const bool once = a.rows * a.H * (bf16 ? 2 : 4) > kLastLevelBytes;
+    if (bf16) {
+        if (once) combine_kernel<uint16_t, true><<<grid, kBlock, 0, stream>>>(a, pieces);
+        else combine_kernel<uint16_t, false><<<grid, kBlock, 0, stream>>>(a, pieces);
+    } else {
+        if (once) combine_kernel<float, true><<<grid, kBlock, 0, stream>>>(a, pieces);
+        else combine_kernel<float, false><<<grid, kBlock, 0, stream>>>(a, pieces);
+    }
     return hipGetLastError();
 }
 
@@ -185,7 +196,10 @@ template <class E, int W, int U>
 static void start_backward(const CombineArgs &a, hipStream_t stream) {
     const int64_t pair_blocks = ceil_div(a.T * a.k, kBlock / W);
     const unsigned grid = (unsigned)(pair_blocks + ceil_div(a.rows, kBlock / 64 * kZeroRows));
-    combine_backward_kernel<E, W, U><<<grid, kBlock, 0, stream>>>(a, pair_blocks);
+    if (2 * a.rows * a.H * (int64_t)sizeof(E) > kLastLevelBytes)
+        combine_backward_kernel<E, W, U, true><<<grid, kBlock, 0, stream>>>(a, pair_blocks);
+    else
+        combine_backward_kernel<E, W, U, false><<<grid, kBlock, 0, stream>>>(a, pair_blocks);
 }
 template <class E>
 static void start_backward(const CombineArgs &a, hipStream_t stream) {

@@ -255,9 +255,11 @@ __device__ __forceinline__ uint64_t *part_keys(const LogprobsArgs &a) {
 }
 
 // One pass over a slice of a row: running maximum, sum and weighted sum per
-// lane, joined over the block.  2048 rows of 131072 bf16 take 91 us, 5.9 TB/s
+// lane, joined over the block.  2048 rows of 131072 bf16 take 88 us, 6.1 TB/s
 // (a large copy moves 5.3): HBM and the vector ALU (9.2 instructions a logit, busy
 // for 94% of the time) are both at their limits; one row of 131072 5.1 us.
+// ONCE: the logits are larger than the last-level cache and are read past it
+// (91.5 us if not; the call and its gradient 263 us instead of 293).
 //
 // The best n: the pass keeps each thread's largest logit only.  n threads'
 // largest reach the n-th largest of them, so no logit below that bar is among
@@ -265,7 +267,7 @@ __device__ __forceinline__ uint64_t *part_keys(const LogprobsArgs &a) {
 // at again (n / BLOCK of the row), those above the bar gathered and ranked.
 // 2048 rows of 131072 bf16 with n = 5: 107 us (a list kept sorted during the
 // pass: 182); one row with n = 20: 12.6 us with the join (22).
-template <class E, bool TOP, int BLOCK>
+template <class E, bool TOP, int BLOCK, bool ONCE>
 __global__ __launch_bounds__(BLOCK) void logprobs_kernel(const LogprobsArgs a) {
     constexpr int kV = Elem<E>::kVec, kWaves = BLOCK / 64;
     __shared__ Stats parts[kWaves];
@@ -293,7 +295,7 @@ __global__ __launch_bounds__(BLOCK) void logprobs_kernel(const LogprobsArgs a) {
         for (; base + U * kStep <= hi; base += U * kStep, col += U * kStep) {
             v4u r[U];
 #pragma unroll
-            for (int u = 0; u < U; ++u) r[u] = load16(row + col + u * kStep);
+            for (int u = 0; u < U; ++u) r[u] = load16<ONCE>(row + col + u * kStep);
             float x[U * kV];
 #pragma unroll
             for (int u = 0; u < U; ++u) Elem<E>::unpack(r[u], x + u * kV);
@@ -391,10 +393,13 @@ __global__ __launch_bounds__(64) void logprobs_join_kernel(const LogprobsArgs a)
 // d logits = (g (1[target] - p) - h p (log p + H)) / temp with g, h the
 // gradients of log-probability and entropy, log p = x / temp - m - log_sum.
 // One read and one write of the logits; in place is fine (a thread writes
-// what it alone has read).  2048 rows of 131072 bf16 take 187 us, 5.75 TB/s,
-// more than a large copy's 5.3.  A row of 9000 in two blocks of equal length
-// 53 us, cut at 8192 72 us (8000 rows).
-template <class E, int BLOCK>
+// what it alone has read).  2048 rows of 131072 bf16 take 174 us, 6.2 TB/s,
+// more than a large copy's 5.3.  ONCE: what is read and written (in place: the
+// logits alone) is larger than the last-level cache and goes past it (187 us
+// if not; but 511 rows of 100003 fp32 written, scored and overwritten in place,
+// which fit, would take 185 us instead of 167).  A row of 9000 in two blocks of equal length 53
+// us, cut at 8192 72 us (8000 rows).
+template <class E, int BLOCK, bool ONCE>
 __global__ __launch_bounds__(BLOCK) void logprobs_backward_kernel(const LogprobsArgs a) {
     constexpr int kV = Elem<E>::kVec, kStep = BLOCK * kV;
     const int64_t t = (int64_t)blockIdx.x / a.slices;
@@ -407,7 +412,7 @@ __global__ __launch_bounds__(BLOCK) void logprobs_backward_kernel(const Logprobs
     v4u r[kUnroll];                                  // a thread's whole share, before anything is written
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u)
-        if (hi - col - u * kStep >= kV) r[u] = load16(row + col + u * kStep);
+        if (hi - col - u * kStep >= kV) r[u] = load16<ONCE>(row + col + u * kStep);
     const int64_t target = a.targets[t];
     const bool real = target >= 0 && target < a.V;
     const float g = real && a.d_logprobs ? a.d_logprobs[t] : 0.0f;
@@ -432,7 +437,7 @@ __global__ __launch_bounds__(BLOCK) void logprobs_backward_kernel(const Logprobs
             x[i] = d;
         }
         if (n >= kV) {
-            store16(out + at, Elem<E>::pack(x));
+            store16<ONCE>(out + at, Elem<E>::pack(x));
         } else {
 #pragma unroll
             for (int i = 0; i < kV; ++i)
@@ -460,15 +465,31 @@ int slices_of(int64_t T, int64_t V, int cus) {
 //   2600 rows of 50001 bf16          50.7 / 50.7 / 48.9 / 51.4 / 59.7
 //   1340 rows of 100003 fp32          105 /  104 /  104 / 98.6 / 96.2
 //   1340 rows of 100003 bf16, n = 5  91.7 / 68.1 / 59.3 / 57.4 / 91.3
-template <class E, bool TOP>
+template <class E, bool TOP, bool ONCE>
 void start(const LogprobsArgs &a, int cus, hipStream_t stream) {
     const unsigned grid = (unsigned)(a.T * a.slices);
     const bool many = a.T >= 4 * cus;
-    if (many && a.slice <= 2048) logprobs_kernel<E, TOP, 64><<<grid, 64, 0, stream>>>(a);
-    else if (many && a.slice <= 8192) logprobs_kernel<E, TOP, 128><<<grid, 128, 0, stream>>>(a);
-    else if (a.slice <= (TOP ? 32768 : 65536)) logprobs_kernel<E, TOP, 256><<<grid, 256, 0, stream>>>(a);
-    else logprobs_kernel<E, TOP, TOP ? 512 : 1024><<<grid, TOP ? 512 : 1024, 0, stream>>>(a);
+    constexpr int wide = TOP ? 512 : 1024;
+    if (many && a.slice <= 2048) logprobs_kernel<E, TOP, 64, ONCE><<<grid, 64, 0, stream>>>(a);
+    else if (many && a.slice <= 8192) logprobs_kernel<E, TOP, 128, ONCE><<<grid, 128, 0, stream>>>(a);
+    else if (a.slice <= (TOP ? 32768 : 65536)) logprobs_kernel<E, TOP, 256, ONCE><<<grid, 256, 0, stream>>>(a);
+    else logprobs_kernel<E, TOP, wide, ONCE><<<grid, wide, 0, stream>>>(a);
     if (a.slices > 1) logprobs_join_kernel<E><<<(unsigned)a.T, 64, 0, stream>>>(a);
+}
+template <class E>
+void start(const LogprobsArgs &a, int cus, hipStream_t stream) {
+    const bool once = a.T * a.V * (int64_t)sizeof(E) > kLastLevelBytes;
+    if (a.top) once ? start<E, true, true>(a, cus, stream) : start<E, true, false>(a, cus, stream);
+    else once ? start<E, false, true>(a, cus, stream) : start<E, false, false>(a, cus, stream);
+}
+template <class E, int BLOCK>
+void start_backward(const LogprobsArgs &a, hipStream_t stream) {
+    const unsigned grid = (unsigned)(a.T * a.slices);
+    const int64_t bytes = a.T * a.V * (int64_t)sizeof(E);
+    if ((a.x == a.dx ? bytes : 2 * bytes) > kLastLevelBytes)
+        logprobs_backward_kernel<E, BLOCK, true><<<grid, BLOCK, 0, stream>>>(a);
+    else
+        logprobs_backward_kernel<E, BLOCK, false><<<grid, BLOCK, 0, stream>>>(a);
 }
 
 }  // namespace
@@ -485,13 +506,8 @@ hipError_t launch_logprobs(LogprobsArgs a, bool bf16, size_t workspace_bytes, hi
     a.slices = slices_of(a.T, a.V, cus);
     if (!a.workspace || (int64_t)workspace_bytes < logprobs_workspace_bytes(a.T, a.V, a.top, cus)) a.slices = 1;
     a.slice = ceil_div(ceil_div(a.V, a.slices), 8) * 8;
-    if (bf16) {
-        if (a.top) start<uint16_t, true>(a, cus, stream);
-        else start<uint16_t, false>(a, cus, stream);
-    } else {
-        if (a.top) start<float, true>(a, cus, stream);
-        else start<float, false>(a, cus, stream);
-    }
+    if (bf16) start<uint16_t>(a, cus, stream);
+    else start<float>(a, cus, stream);
     return hipGetLastError();
 }
 
@@ -505,14 +521,8 @@ hipError_t launch_logprobs_backward(LogprobsArgs a, bool bf16, hipStream_t strea
     const int64_t most = kUnroll * vec * (narrow ? 64 : kBlock);
     a.slices = (int)ceil_div(a.V, most);
     a.slice = ceil_div(ceil_div(a.V, a.slices), vec) * vec;
-    const unsigned grid = (unsigned)(a.T * a.slices);
-    if (narrow) {
-        if (bf16) logprobs_backward_kernel<uint16_t, 64><<<grid, 64, 0, stream>>>(a);
-        else logprobs_backward_kernel<float, 64><<<grid, 64, 0, stream>>>(a);
-    } else {
-        if (bf16) logprobs_backward_kernel<uint16_t, kBlock><<<grid, kBlock, 0, stream>>>(a);
-        else logprobs_backward_kernel<float, kBlock><<<grid, kBlock, 0, stream>>>(a);
-    }
+    if (bf16) narrow ? start_backward<uint16_t, 64>(a, stream) : start_backward<uint16_t, kBlock>(a, stream);
+    else narrow ? start_backward<float, 64>(a, stream) : start_backward<float, kBlock>(a, stream);
     return hipGetLastError();
 }
 

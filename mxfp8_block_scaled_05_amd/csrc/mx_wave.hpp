@@ -86,6 +86,29 @@ __device__ __forceinline__ void store16(P *p, v4u v) {
     reinterpret_cast<Bytes16 *>(p)->v = v;
 }
 
+// The same with ONCE for data that a pass reads or writes once and that is too
+// large to stay in the last-level cache: nontemporal, so that it does not push
+// through the caches.
+constexpr int64_t kLastLevelBytes = 256 << 20;
+template <class P>
+struct Once16 {
+    typedef uint32_t type __attribute__((ext_vector_type(4), aligned(4)));
+};
+template <>
+struct Once16<uint16_t> {
+    typedef uint32_t type __attribute__((ext_vector_type(4), aligned(2)));
+};
+template <bool ONCE, class P>
+__device__ __forceinline__ v4u load16(const P *p) {
+    if constexpr (ONCE) return __builtin_nontemporal_load(reinterpret_cast<const typename Once16<P>::type *>(p));
+    else return load16(p);
+}
+template <bool ONCE, class P>
+__device__ __forceinline__ void store16(P *p, v4u v) {
+    if constexpr (ONCE) __builtin_nontemporal_store(v, reinterpret_cast<typename Once16<P>::type *>(p));
+    else store16(p, v);
+}
+
 // Element types of the calls: fp32, or bf16 as its bit pattern.
 template <class E>
 struct Elem;

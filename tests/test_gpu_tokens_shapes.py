@@ -95,3 +95,44 @@ def test_route_far_rows(mx):
     dw = torch.randn(w.shape, generator=g, device="cuda")
     d = mx.route_backward(x, ids, dw)
     assert torch.equal(d[-200:], mx.route_backward(x[-200:].contiguous(), tail_ids, dw[-200:].contiguous()))
+
+
+@pytest.mark.parametrize("dtype,V", [(torch.float32, 100001), (torch.bfloat16, 200003)])
+def test_logprobs_larger_than_the_cache(mx, dtype, V):
+    """Logits of more than 256 MB: the rows' results are those of a call on a part of them."""
+    print("large logits", dtype, V, flush=True)
+    x, t = _inputs(720, V, dtype, V)
+    for n in (0, 6):
+        a, b = mx.token_logprobs(x, t, top_n=n), mx.token_logprobs(x[:300], t[:300], top_n=n)
+        for p, q in ((a.logprobs, b.logprobs), (a.entropy, b.entropy), (a.stats, b.stats)) + (
+                ((a.top_logprobs, b.top_logprobs), (a.top_ids, b.top_ids)) if n else ()):
+            assert torch.equal(p[:300], q)
+    g = torch.randn(720, device="cuda")
+    d = mx.token_logprobs_backward(x, t, a.stats, a.entropy, g, g)
+    part = mx.token_logprobs_backward(x[:150], t[:150], a.stats[:150], a.entropy[:150], g[:150], g[:150])
+    assert torch.equal(d[:150], part)
+    assert mx.token_logprobs_backward(x, t, a.stats, a.entropy, g, g, out=x) is x and torch.equal(x, d)
+
+
+@pytest.mark.parametrize("dtype,H", [(torch.float32, 2048), (torch.float32, 1021), (torch.bfloat16, 4099), (torch.bfloat16, 120)])
+def test_combine_larger_than_the_cache(mx, dtype, H):
+    print("large rows", dtype, H, flush=True)
+    size = 2 if dtype is torch.bfloat16 else 4
+    rows = (300 << 20) // (H * size)
+    y = torch.randn((rows, H), device="cuda").to(dtype)
+    T = 500
+    at = torch.randperm(rows, device="cuda")[:2 * T].view(T, 2).int()
+    w = torch.tensor([0.5, -2.0], device="cuda").expand(T, 2).contiguous()
+    out = mx.moe_combine(y, at, w)
+    d = torch.randn((T, H), device="cuda").to(dtype)
+    row_token = torch.full((rows,), -1, dtype=torch.int64, device="cuda")
+    row_token[at.long().view(-1)] = torch.arange(T, device="cuda").repeat_interleave(2)
+    dy, dw = mx.moe_combine_backward(d, y, at, w, row_token)
+    # the same rows in a small matrix
+    small = torch.arange(2 * T, device="cuda").view(T, 2).int()
+    ys = y[at.long().view(-1)].contiguous()
+    assert torch.equal(out, mx.moe_combine(ys, small, w))
+    dys, dws = mx.moe_combine_backward(d, ys, small, w, torch.arange(T, device="cuda").repeat_interleave(2))
+    assert torch.equal(dw, dws) and torch.equal(dy[at.long().view(-1)], dys)
+    dy[at.long().view(-1)] = 0
+    assert not dy.any()
