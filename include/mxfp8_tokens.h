@@ -168,7 +168,9 @@ mxfp8_status mxfp8_token_logprobs(const void *logits, mxfp8_dtype dtype, int64_t
  *   temperature, g = d_logprobs[t] (0 where the target is outside [0, V)),
  *   h = d_entropy[t]; a term whose gradient is NULL is left out (not both;
  *   entropy may be NULL with d_entropy).  Columns of -Inf get 0 (the
- *   target's g / temperature).
+ *   target's g / temperature).  A row whose L is NaN (a NaN or +Inf among its
+ *   logits, or nothing above -Inf) gets NaN in every column, whatever g and h
+ *   are.
  *   stats and entropy as mxfp8_token_logprobs gave them for the same logits
  *   and temperature.  d_logits: rows ld_out >= V apart, in the logits' dtype;
  *   it may be the logits themselves (same pointer and ld).

@@ -420,7 +420,9 @@ __global__ __launch_bounds__(BLOCK) void logprobs_backward_kernel(const Logprobs
     const float H = h != 0.0f ? a.entropy[t] : 0.0f;
     const float m = a.stats[2 * t], log_sum = a.stats[2 * t + 1];
     const float inv = a.inv, inv_low = a.inv_low;                            // 1 / temp = inv + inv_low
-    const float c0 = -(g + h * H) * inv, c1 = -h * inv, at_target = g * inv;
+    // L is NaN in a row without statistics (a NaN or +Inf in it, or nothing above -Inf): c0 takes that to every
+    // column, since the lower limit of log p, which stands for -Inf columns, drops a NaN
+    const float c0 = -(g + h * H) * inv + (log_sum - log_sum), c1 = -h * inv, at_target = g * inv;
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
         const int64_t at = col + u * kStep, n = hi - at;
