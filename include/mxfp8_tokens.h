@@ -139,7 +139,8 @@ size_t mxfp8_token_logprobs_workspace_bytes(int64_t T, int64_t V, int64_t top_n)
  *   z = x / temperature, m = max z, L = log sum e^(z - m), log p = z - m - L
  *   logprobs[t] = log p[targets[t]], 0 for a target outside [0, V)
  *   entropy[t]  = -sum p log p (terms with p = 0 are 0)
- *   stats[t]    = (m, L), what the gradient needs
+ *   stats[t]    = (m, L), what the gradient needs: m rounded to fp32 (finite
+ *     logits: to a finite number) and, while |m| < 2^31, L to that m
  *   top_ids[t][0..top_n), top_logprobs: the columns of the largest logits,
  *     largest first, the lower column first among equals, and their log p
  * Logits of -Inf are tokens that cannot occur; a row of nothing else has
@@ -170,7 +171,8 @@ mxfp8_status mxfp8_token_logprobs(const void *logits, mxfp8_dtype dtype, int64_t
  *   entropy may be NULL with d_entropy).  Columns of -Inf get 0 (the
  *   target's g / temperature).  A row whose L is NaN (a NaN or +Inf among its
  *   logits, or nothing above -Inf) gets NaN in every column, whatever g and h
- *   are.
+ *   are.  Where |m| >= 2^31, logits whose z rounds to m in fp32 have p = e^-L
+ *   and the others 0 (rows of the type's lowest value: the same p for all).
  *   stats and entropy as mxfp8_token_logprobs gave them for the same logits
  *   and temperature.  d_logits: rows ld_out >= V apart, in the logits' dtype;
  *   it may be the logits themselves (same pointer and ld).

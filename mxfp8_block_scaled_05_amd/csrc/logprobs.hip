@@ -12,6 +12,14 @@ namespace {
 constexpr int kBlock = 256;         // threads of the gradient's blocks
 constexpr int kUnroll = 4;          // 16-byte loads of a thread in flight
 constexpr float kLowest = -3.402823466e38f;
+// From here on different fp32 logits have z at least 2^7 apart: e^-128 is 0.
+constexpr float kFar = 0x1p31f;
+
+// z = x / temperature rounded to fp32; finite logits stay finite
+__device__ __forceinline__ float scaled(float x, double inv_temperature) {
+    const double z = x * inv_temperature;
+    return __builtin_isinf(x) ? x : z > -kLowest ? -kLowest : z < kLowest ? kLowest : (float)z;
+}
 
 // Statistics of a set of logits: m = max x, s = sum e^((x - m) / temp),
 // w = sum e^(..) (x - m) c with c = log2(e) / temp (so w is in base 2).
@@ -237,8 +245,10 @@ __device__ __forceinline__ void finish_row(const LogprobsArgs &a, int64_t t, con
     if (lane == 0) {
         a.logprobs[t] = target.real ? (float)(((double)target.x - top) * a.inv_temperature - log_sum) : 0.0f;
         a.entropy[t] = none ? __builtin_nanf("") : log_sum - v.w / v.s * kLn2;
-        a.stats[2 * t] = (float)(top * a.inv_temperature);
-        a.stats[2 * t + 1] = log_sum;
+        // L against the rounded m, so that the gradient's z - m - L loses nothing by that rounding
+        const float m = scaled(top, a.inv_temperature);
+        a.stats[2 * t] = m;
+        a.stats[2 * t + 1] = __builtin_fabsf(m) < kFar ? (float)(log_sum + (top * a.inv_temperature - m)) : log_sum;
     }
     if (lane < a.top) {
         a.top_ids[t * a.top + lane] = (uint32_t)~(uint32_t)list;
@@ -390,6 +400,30 @@ __global__ __launch_bounds__(64) void logprobs_join_kernel(const LogprobsArgs a)
     finish_row(a, t, v, target, list, lane);
 }
 
+// A row's distances z - m as x (by + by_low) - from, and a bound of log p.
+struct Line {
+    float by, by_low, from, most;
+};
+
+// The line of a row with |m| >= kFar.  A distance there is 0 or far below -128
+// and what x loses in z's rounding more than either, so the line starts at the
+// smallest logit whose z rounds to m, is steep enough to take every lower one
+// (2^-24 of it away at least) to p = 0, and log p ends at -L.
+__device__ __forceinline__ Line far_line(const LogprobsArgs &a, float m, float log_sum) {
+    const double at = (double)m * a.temperature;                 // within 2 steps of fp32 of that logit
+    float x = at > -kLowest ? -kLowest : at < kLowest || m <= kLowest ? kLowest : (float)at;
+    const uint32_t down = m < 0.0f ? 1u : -1u;
+    for (int i = 0; i < 3; ++i) {
+        const float lower = __uint_as_float(__float_as_uint(x) + down);
+        if (lower >= kLowest && scaled(lower, a.inv_temperature) == m) x = lower;
+    }
+    for (int i = 0; i < 3; ++i)
+        if (scaled(x, a.inv_temperature) < m) x = __uint_as_float(__float_as_uint(x) - down);
+    const int exponent = (int)((__float_as_uint(x) >> 23) & 255) - 127;
+    const float by = __builtin_ldexpf(1.0f, 40 - exponent);      // x * by: 2^40 to 2^41
+    return {by, 0.0f, x * by, -log_sum};
+}
+
 // d logits = (g (1[target] - p) - h p (log p + H)) / temp with g, h the
 // gradients of log-probability and entropy, log p = x / temp - m - log_sum.
 // One read and one write of the logits; in place is fine (a thread writes
@@ -423,6 +457,8 @@ __global__ __launch_bounds__(BLOCK) void logprobs_backward_kernel(const Logprobs
     // L is NaN in a row without statistics (a NaN or +Inf in it, or nothing above -Inf): c0 takes that to every
     // column, since the lower limit of log p, which stands for -Inf columns, drops a NaN
     const float c0 = -(g + h * H) * inv + (log_sum - log_sum), c1 = -h * inv, at_target = g * inv;
+    Line line{inv, inv_low, m, 1000.0f};
+    if (__builtin_fabsf(m) >= kFar) line = far_line(a, m, log_sum);
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
         const int64_t at = col + u * kStep, n = hi - at;
@@ -432,7 +468,9 @@ __global__ __launch_bounds__(BLOCK) void logprobs_backward_kernel(const Logprobs
         else load_head<kV>(row + at, (int)n, 0.0f, x);
 #pragma unroll
         for (int i = 0; i < kV; ++i) {
-            const float logp = __builtin_fmaxf(__builtin_fmaf(x[i], inv, __builtin_fmaf(x[i], inv_low, -m)) - log_sum, -1000.0f);
+            // one rounding of x * by - from, which is about as large as the distance: z itself is never rounded
+            const float z = __builtin_fmaf(x[i], line.by_low, __builtin_fmaf(x[i], line.by, -line.from));
+            const float logp = __builtin_amdgcn_fmed3f(z - log_sum, -1000.0f, line.most);
             const float p = __builtin_amdgcn_exp2f(logp * kLog2E);
             float d = p * __builtin_fmaf(c1, logp, c0);
             if (at + i == target) d += at_target;
