@@ -14,7 +14,8 @@
  * synchronization, graph-capturable, deterministic), except for alignment:
  * every pointer here needs only its element's own (2 bytes for bf16, 4 for
  * fp32 and int32, 8 for int64), MXFP8_ERR_ALIGN otherwise, so views that
- * start at any row or column are fine.  Sums, softmax statistics and
+ * start at any row or column are fine, and rows may lie any number of elements
+ * apart (T * ld <= 2^60).  Sums, softmax statistics and
  * gradients are computed in fp32 and rounded once on output.
  */
 #ifndef MXFP8_TOKENS_H

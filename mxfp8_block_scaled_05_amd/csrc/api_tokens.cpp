@@ -15,6 +15,8 @@ constexpr int64_t kMaxInt = (int64_t)1 << 31;
 
 // a * b < 2^31 for a, b >= 0
 bool product_ok(int64_t a, int64_t b) { return a == 0 || b <= (kMaxInt - 1) / a; }
+// rows of `cols` elements ld apart, with byte offsets that fit 63 bits
+bool rows_ok(int64_t T, int64_t cols, int64_t ld) { return ld >= cols && (T == 0 || ld <= ((int64_t)1 << 60) / T); }
 bool aligned(const void *p, size_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
 bool dtype_ok(const mxfp8_dtype &d) { return raw(d) == MXFP8_F32 || raw(d) == MXFP8_BF16; }
 bool score_ok(const mxfp8_score &s) { return raw(s) == MXFP8_SCORE_SOFTMAX || raw(s) == MXFP8_SCORE_SIGMOID; }
@@ -25,8 +27,8 @@ bool temperature_ok(double t) { return t >= 0x1p-60 && t <= 0x1p60; }   // 1 / t
 bool grid_ok(int64_t blocks) { return blocks < ((int64_t)1 << 24); }
 
 bool route_sizes_ok(int64_t ld, int64_t T, int64_t E, int64_t k) {
-    return T >= 0 && T < kMaxInt && E >= 1 && E <= kRouteMaxExperts && k >= 1 && k <= kRouteMaxK && k <= E && ld >= E &&
-           ld < kMaxInt && grid_ok(ceil_div(T, 4));
+    return T >= 0 && T < kMaxInt && E >= 1 && E <= kRouteMaxExperts && k >= 1 && k <= kRouteMaxK && k <= E &&
+           rows_ok(T, E, ld) && grid_ok(ceil_div(T, 4));
 }
 
 }  // namespace
@@ -171,7 +173,7 @@ mxfp8_status mxfp8_token_logprobs(const void *logits, mxfp8_dtype dtype, int64_t
                                   float *entropy, float *stats, float *top_logprobs, int64_t *top_ids,
                                   void *workspace, size_t workspace_bytes, hipStream_t stream) {
     if (!dtype_ok(dtype)) return MXFP8_ERR_DTYPE;
-    if (!logprobs_sizes_ok(T, V) || ld < V || ld >= kMaxInt || top_n < 0 || top_n > kLogprobsMaxTop || top_n > V)
+    if (!logprobs_sizes_ok(T, V) || !rows_ok(T, V, ld) || top_n < 0 || top_n > kLogprobsMaxTop || top_n > V)
         return MXFP8_ERR_SHAPE;
     if (!temperature_ok(temperature)) return MXFP8_ERR_SHAPE;
     if (T == 0) return MXFP8_OK;
@@ -194,7 +196,7 @@ mxfp8_status mxfp8_token_logprobs_backward(const void *logits, mxfp8_dtype dtype
                                            const float *d_logprobs, const float *d_entropy, double temperature,
                                            void *d_logits, int64_t ld_out, hipStream_t stream) {
     if (!dtype_ok(dtype)) return MXFP8_ERR_DTYPE;
-    if (!logprobs_sizes_ok(T, V) || ld < V || ld >= kMaxInt || ld_out < V || ld_out >= kMaxInt) return MXFP8_ERR_SHAPE;
+    if (!logprobs_sizes_ok(T, V) || !rows_ok(T, V, ld) || !rows_ok(T, V, ld_out)) return MXFP8_ERR_SHAPE;
     if (!temperature_ok(temperature)) return MXFP8_ERR_SHAPE;
     if (T == 0) return MXFP8_OK;
     if (!logits || !targets || !stats || !d_logits || (!d_logprobs && !d_entropy) || (d_entropy && !entropy))
