@@ -47,7 +47,9 @@ typedef enum {
     MXFP8_ERR_DTYPE = 4,       /* unknown output dtype or B layout                    */
     MXFP8_ERR_ALIGN = 5,       /* a pointer is not 16-byte aligned                    */
     MXFP8_ERR_HIP = 6,         /* a HIP launch or query failed                        */
-    MXFP8_ERR_UNSUPPORTED = 7  /* the current device is not gfx950                    */
+    MXFP8_ERR_UNSUPPORTED = 7, /* the current device is not gfx950                    */
+    MXFP8_ERR_OVERLAP = 8      /* an output overlaps another buffer of the call
+                                  (checked by the calls of mxfp8_tokens.h)           */
 } mxfp8_status;
 
 typedef enum { MXFP8_F32 = 0, MXFP8_BF16 = 1 } mxfp8_dtype;

@@ -15,7 +15,9 @@
  * every pointer here needs only its element's own (2 bytes for bf16, 4 for
  * fp32 and int32, 8 for int64), MXFP8_ERR_ALIGN otherwise, so views that
  * start at any row or column are fine, and rows may lie any number of elements
- * apart (T * ld <= 2^60).  Sums, softmax statistics and
+ * apart (T * ld <= 2^60).  An output that shares memory with an input or with
+ * another output is refused (MXFP8_ERR_OVERLAP) except where a call names it;
+ * strided rows may lie between each other's.  Sums, softmax statistics and
  * gradients are computed in fp32 and rounded once on output.
  */
 #ifndef MXFP8_TOKENS_H
@@ -67,7 +69,7 @@ mxfp8_status mxfp8_route(const void *logits, mxfp8_dtype dtype, int64_t ld, int6
  *
  *   d_logits [T][E] in the logits' dtype, all of it written; ids as
  *   mxfp8_route gives them (distinct within a token; an id outside [0, E) is
- *   no expert).  Limits as mxfp8_route's.  d_logits must not overlap logits.
+ *   no expert).  Limits as mxfp8_route's.
  */
 mxfp8_status mxfp8_route_backward(const void *logits, mxfp8_dtype dtype, int64_t ld, int64_t T, int64_t E,
                                   int64_t k, mxfp8_score score, const int32_t *ids, const float *d_weights,
@@ -109,8 +111,8 @@ mxfp8_status mxfp8_route_tables(const int32_t *ids, int64_t T, int64_t k, int64_
  * mxfp8_moe_combine -- out[t] = sum_j weights[t][j] * y[pair_row[t][j]], added
  * in the order of j.  y [rows][H] and out [T][H] FP32 or BF16; a pair_row
  * outside [0, rows) adds nothing (a token with no rows gets zeros).
- * T, rows >= 0 (T = 0 enqueues nothing), H, k >= 1, T * k < 2^26,
- * T * ceil(H / 4) < 2^31.
+ * T, rows >= 0 (T = 0 enqueues nothing), H, k >= 1, T * k + rows / 8 < 2^26,
+ * T * ceil(H / 4) < 2^31, rows * H <= 2^60.
  */
 mxfp8_status mxfp8_moe_combine(const void *y, mxfp8_dtype dtype, int64_t rows, int64_t H, const int32_t *pair_row,
                                const float *weights, int64_t T, int64_t k, void *out, hipStream_t stream);
@@ -123,7 +125,8 @@ mxfp8_status mxfp8_moe_combine(const void *y, mxfp8_dtype dtype, int64_t rows, i
  *     outside [0, rows)
  * pair_row and row_token are one mxfp8_route_tables result: each row belongs
  * to one pair or to none (rows of other tables are left unspecified, never
- * addressed outside the buffers).  Limits as mxfp8_moe_combine's.
+ * addressed outside the buffers).  d_y may be y and d_weights the weights
+ * (same pointers).  Limits as mxfp8_moe_combine's.
  */
 mxfp8_status mxfp8_moe_combine_backward(const void *d_out, const void *y, mxfp8_dtype dtype, int64_t rows, int64_t H,
                                         const int32_t *pair_row, const float *weights, const int64_t *row_token,

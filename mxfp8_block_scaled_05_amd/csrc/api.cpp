@@ -109,9 +109,10 @@ const char *mxfp8_status_string(mxfp8_status s) {
         case MXFP8_ERR_SHAPE: return "MXFP8_ERR_SHAPE: invalid or unsupported size";
         case MXFP8_ERR_AXIS: return "MXFP8_ERR_AXIS: axis must be 0 or 1";
         case MXFP8_ERR_DTYPE: return "MXFP8_ERR_DTYPE: unknown dtype or layout";
-        case MXFP8_ERR_ALIGN: return "MXFP8_ERR_ALIGN: pointer not 16-byte aligned";
+        case MXFP8_ERR_ALIGN: return "MXFP8_ERR_ALIGN: pointer not aligned (16 bytes; token-level calls: its element's size)";
         case MXFP8_ERR_HIP: return "MXFP8_ERR_HIP: HIP launch or query failed";
         case MXFP8_ERR_UNSUPPORTED: return "MXFP8_ERR_UNSUPPORTED: device is not gfx950";
+        case MXFP8_ERR_OVERLAP: return "MXFP8_ERR_OVERLAP: an output overlaps another buffer of the call";
     }
     return "MXFP8: unknown status";
 }

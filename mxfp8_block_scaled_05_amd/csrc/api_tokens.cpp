@@ -4,6 +4,8 @@
 
 #include <hip/hip_runtime.h>
 
+#include <initializer_list>
+
 #include "mx_api.hpp"
 #include "mx_launch.hpp"
 
@@ -22,13 +24,53 @@ bool dtype_ok(const mxfp8_dtype &d) { return raw(d) == MXFP8_F32 || raw(d) == MX
 bool score_ok(const mxfp8_score &s) { return raw(s) == MXFP8_SCORE_SOFTMAX || raw(s) == MXFP8_SCORE_SIGMOID; }
 size_t elem_bytes(const mxfp8_dtype &d) { return raw(d) == MXFP8_BF16 ? 2 : 4; }
 
-// workgroups of 256 threads whose threads must stay below 2^32
 bool temperature_ok(double t) { return t >= 0x1p-60 && t <= 0x1p60; }   // 1 / t stays an fp32 number
+// workgroups of 256 threads whose threads must stay below 2^32
 bool grid_ok(int64_t blocks) { return blocks < ((int64_t)1 << 24); }
 
 bool route_sizes_ok(int64_t ld, int64_t T, int64_t E, int64_t k) {
     return T >= 0 && T < kMaxInt && E >= 1 && E <= kRouteMaxExperts && k >= 1 && k <= kRouteMaxK && k <= E &&
            rows_ok(T, E, ld) && grid_ok(ceil_div(T, 4));
+}
+
+// A buffer: `rows` rows of `bytes` bytes, `step` bytes apart.
+struct Span {
+    uintptr_t at;
+    int64_t rows, bytes, step;
+    Span(const void *p, int64_t n) : at((uintptr_t)p), rows(1), bytes(n), step(n) {}
+    Span(const void *p, int64_t rows_, int64_t n, int64_t step_) : at((uintptr_t)p), rows(rows_), bytes(n), step(step_) {}
+    bool empty() const { return !at || rows <= 0 || bytes <= 0; }
+    uintptr_t end() const { return at + (rows - 1) * step + bytes; }
+};
+
+// Whether rows of a and b, both step bytes apart, share a byte: b's row j meets
+// a's row i if j - i lies between two bounds that follow from the distance.
+bool rows_meet(const Span &a, const Span &b, int64_t step) {
+    const int64_t d = (int64_t)(a.at - b.at);
+    const int64_t above = d - b.bytes, below = d + a.bytes;          // above < (j - i) * step < below
+    const int64_t lo = above >= 0 ? above / step + 1 : -((-above - 1) / step);
+    const int64_t hi = below > 0 ? (below - 1) / step : -(-below / step) - 1;
+    return (lo > 1 - a.rows ? lo : 1 - a.rows) <= (hi < b.rows - 1 ? hi : b.rows - 1);
+}
+bool meet(const Span &a, const Span &b) {
+    if (a.empty() || b.empty() || a.end() <= b.at || b.end() <= a.at) return false;
+    if (a.rows == 1 || a.step == b.step) return rows_meet(a, b, b.step);
+    if (b.rows == 1) return rows_meet(b, a, a.step);
+    if (a.rows > b.rows) return meet(b, a);
+    for (int64_t i = 0; i < a.rows; ++i)
+        if (rows_meet(Span(reinterpret_cast<const void *>(a.at + i * a.step), a.bytes), b, b.step)) return true;
+    return false;
+}
+
+// Whether an output shares a byte with an input or with another output.
+bool overlap(std::initializer_list<Span> outputs, std::initializer_list<Span> inputs) {
+    for (const Span *o = outputs.begin(); o != outputs.end(); ++o) {
+        for (const Span &i : inputs)
+            if (meet(*o, i)) return true;
+        for (const Span *q = o + 1; q != outputs.end(); ++q)
+            if (meet(*o, *q)) return true;
+    }
+    return false;
 }
 
 }  // namespace
@@ -49,6 +91,9 @@ mxfp8_status mxfp8_route(const void *logits, mxfp8_dtype dtype, int64_t ld, int6
     if (!logits || !ids || !weights) return MXFP8_ERR_NULL;
     if (!aligned(logits, elem_bytes(dtype)) || !aligned(bias, 4) || !aligned(ids, 4) || !aligned(weights, 4))
         return MXFP8_ERR_ALIGN;
+    const int64_t e = elem_bytes(dtype);
+    if (overlap({{ids, T * k * 4}, {weights, T * k * 4}}, {{logits, T, E * e, ld * e}, {bias, E * 4}}))
+        return MXFP8_ERR_OVERLAP;
     mxfp8_status st = check_device();
     if (st != MXFP8_OK) return st;
     RouteArgs a{};
@@ -68,6 +113,9 @@ mxfp8_status mxfp8_route_backward(const void *logits, mxfp8_dtype dtype, int64_t
     if (!aligned(logits, elem_bytes(dtype)) || !aligned(d_logits, elem_bytes(dtype)) || !aligned(ids, 4) ||
         !aligned(d_weights, 4))
         return MXFP8_ERR_ALIGN;
+    const int64_t e = elem_bytes(dtype);
+    if (overlap({{d_logits, T * E * e}}, {{logits, T, E * e, ld * e}, {ids, T * k * 4}, {d_weights, T * k * 4}}))
+        return MXFP8_ERR_OVERLAP;
     mxfp8_status st = check_device();
     if (st != MXFP8_OK) return st;
     RouteArgs a{};
@@ -101,6 +149,10 @@ mxfp8_status mxfp8_route_tables(const int32_t *ids, int64_t T, int64_t k, int64_
     if (!aligned(ids, 4) || !aligned(offsets, 4) || !aligned(counts, 4) || !aligned(row_token, 8) ||
         !aligned(pair_row, 4) || !aligned(workspace, 4))
         return MXFP8_ERR_ALIGN;
+    const int64_t pairs = T * k;
+    if (overlap({{offsets, (E + 1) * 4}, {counts, E * 4}, {row_token, rows * 8}, {pair_row, pairs * 4}, {workspace, (int64_t)need}},
+                {{ids, pairs * 4}}))
+        return MXFP8_ERR_OVERLAP;
     mxfp8_status st = check_device();
     if (st != MXFP8_OK) return st;
     RouteTables a{};
@@ -111,7 +163,8 @@ mxfp8_status mxfp8_route_tables(const int32_t *ids, int64_t T, int64_t k, int64_
 }
 
 static mxfp8_status combine_sizes(int64_t rows, int64_t H, int64_t T, int64_t k) {
-    if (rows < 0 || rows >= kMaxInt || H < 1 || H >= kMaxInt || T < 0 || T >= kMaxInt || k < 1 || !product_ok(T, k))
+    if (rows < 0 || rows >= kMaxInt || H < 1 || H >= kMaxInt || T < 0 || T >= kMaxInt || k < 1 || !product_ok(T, k) ||
+        !rows_ok(rows, H, H))
         return MXFP8_ERR_SHAPE;
     // a thread per 4 elements of an output row; a wave per pair and per 8 rows
     if (!product_ok(T, ceil_div(H, 4)) || !grid_ok(ceil_div(T * ceil_div(H, 4), 256)) ||
@@ -130,6 +183,9 @@ mxfp8_status mxfp8_moe_combine(const void *y, mxfp8_dtype dtype, int64_t rows, i
     if (!aligned(y, elem_bytes(dtype)) || !aligned(out, elem_bytes(dtype)) || !aligned(pair_row, 4) ||
         !aligned(weights, 4))
         return MXFP8_ERR_ALIGN;
+    const int64_t line = H * (int64_t)elem_bytes(dtype);
+    if (overlap({{out, T, line, line}}, {{y, rows, line, line}, {pair_row, T * k * 4}, {weights, T * k * 4}}))
+        return MXFP8_ERR_OVERLAP;
     st = check_device();
     if (st != MXFP8_OK) return st;
     CombineArgs a{};
@@ -150,6 +206,12 @@ mxfp8_status mxfp8_moe_combine_backward(const void *d_out, const void *y, mxfp8_
     if (!aligned(d_out, e) || !aligned(y, e) || !aligned(d_y, e) || !aligned(pair_row, 4) || !aligned(weights, 4) ||
         !aligned(d_weights, 4) || !aligned(row_token, 8))
         return MXFP8_ERR_ALIGN;
+    // a pair's row of y and its weight are read by the lanes that write its row of d_y and its d_weights alone
+    const int64_t line = H * (int64_t)e, pairs = T * k;
+    if (overlap({{d_y, rows, line, line}, {d_weights, pairs * 4}},
+                {{y == d_y ? nullptr : y, rows, line, line}, {weights == d_weights ? nullptr : weights, pairs * 4},
+                 {d_out, T, line, line}, {pair_row, pairs * 4}, {row_token, rows * 8}}))
+        return MXFP8_ERR_OVERLAP;
     st = check_device();
     if (st != MXFP8_OK) return st;
     CombineArgs a{};
@@ -182,6 +244,12 @@ mxfp8_status mxfp8_token_logprobs(const void *logits, mxfp8_dtype dtype, int64_t
     if (!aligned(logits, elem_bytes(dtype)) || !aligned(targets, 8) || !aligned(logprobs, 4) || !aligned(entropy, 4) ||
         !aligned(stats, 4) || !aligned(top_logprobs, 4) || !aligned(top_ids, 8) || !aligned(workspace, 16))
         return MXFP8_ERR_ALIGN;
+    const int64_t e = elem_bytes(dtype);
+    const int64_t used = workspace ? logprobs_workspace_bytes(T, V, (int)top_n, device_cu_count()) : 0;
+    if (overlap({{logprobs, T * 4}, {entropy, T * 4}, {stats, T * 8}, {top_logprobs, T * top_n * 4}, {top_ids, T * top_n * 8},
+                 {workspace, (int64_t)workspace_bytes < used ? 0 : used}},
+                {{logits, T, V * e, ld * e}, {targets, T * 8}}))
+        return MXFP8_ERR_OVERLAP;
     mxfp8_status st = check_device();
     if (st != MXFP8_OK) return st;
     LogprobsArgs a{};
@@ -206,6 +274,10 @@ mxfp8_status mxfp8_token_logprobs_backward(const void *logits, mxfp8_dtype dtype
     if (!aligned(logits, e) || !aligned(d_logits, e) || !aligned(targets, 8) || !aligned(stats, 4) ||
         !aligned(entropy, 4) || !aligned(d_logprobs, 4) || !aligned(d_entropy, 4))
         return MXFP8_ERR_ALIGN;
+    if (overlap({{d_logits, T, (int64_t)(V * e), (int64_t)(ld_out * e)}},
+                {{logits == d_logits ? nullptr : logits, T, (int64_t)(V * e), (int64_t)(ld * e)}, {targets, T * 8},
+                 {stats, T * 8}, {entropy, T * 4}, {d_logprobs, T * 4}, {d_entropy, T * 4}}))
+        return MXFP8_ERR_OVERLAP;
     mxfp8_status st = check_device();
     if (st != MXFP8_OK) return st;
     LogprobsArgs a{};

@@ -62,7 +62,8 @@ def token_logprobs_backward(logits: torch.Tensor, targets: torch.Tensor, stats: 
                             out: torch.Tensor | None = None) -> torch.Tensor:
     """Gradient of token_logprobs' logprobs and entropy with respect to the
     logits, in their dtype (mxfp8_token_logprobs_backward).  Either gradient
-    may be None.  ``out`` may be the logits themselves (in place)."""
+    may be None.  ``out`` may be the logits themselves (in place), but share no
+    memory with them otherwise."""
     code, ld, T, V, tg, dev = _logits_targets(logits, targets)
     if d_logprobs is None and d_entropy is None:
         raise ValueError("give d_logprobs, d_entropy or both")

@@ -130,7 +130,8 @@ def _combine_args(y, pair_row, weights):
 def moe_combine(y: torch.Tensor, pair_row: torch.Tensor, weights: torch.Tensor,
                 out: torch.Tensor | None = None) -> torch.Tensor:
     """out[t] = sum_j weights[t, j] * y[pair_row[t, j]] in fp32, rounded once
-    to y's dtype (mxfp8_moe_combine).  y fp32 or bf16 [rows, H]."""
+    to y's dtype (mxfp8_moe_combine).  y fp32 or bf16 [rows, H]; ``out`` must not
+    share memory with it."""
     code, p, w = _combine_args(y, pair_row, weights)
     T, k = pair_row.shape
     rows, H = y.shape

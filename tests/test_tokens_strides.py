@@ -22,10 +22,10 @@ def L():
 def _calls(L, ld):
     buf = ctypes.create_string_buffer(4096)
     p = ctypes.c_void_p((ctypes.addressof(buf) + 15) & ~15)
-    o = ctypes.c_void_p(p.value + 2048)
-    yield L.mxfp8_route(p, 1, ld, 2, 64, 4, 0, None, 1, 1, 1, 1, 1.0, o, o, None)
+    o, o2, o3 = (ctypes.c_void_p(p.value + n) for n in (2048, 2560, 3072))
+    yield L.mxfp8_route(p, 1, ld, 2, 64, 4, 0, None, 1, 1, 1, 1, 1.0, o, o2, None)
     yield L.mxfp8_route_backward(p, 1, ld, 2, 64, 4, 0, p, p, 1, 1.0, o, None)
-    yield L.mxfp8_token_logprobs(p, 1, ld, 2, 64, p, 1.0, 0, o, o, o, None, None, None, 0, None)
+    yield L.mxfp8_token_logprobs(p, 1, ld, 2, 64, p, 1.0, 0, o, o2, o3, None, None, None, 0, None)
     yield L.mxfp8_token_logprobs_backward(p, 1, ld, 2, 64, p, p, p, p, p, 1.0, o, 64, None)
     yield L.mxfp8_token_logprobs_backward(p, 1, 64, 2, 64, p, p, p, p, p, 1.0, o, ld, None)
 
