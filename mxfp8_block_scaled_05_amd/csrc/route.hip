@@ -451,7 +451,7 @@ __global__ __launch_bounds__(kBlock) void route_backward_kernel(const RouteArgs 
         ga = group_reduce<L>(id >= 0 ? g * chosen : 0.0f, OpAdd());
     }
     wave_sync();
-    if (id >= 0) full[slot][id] = a.sigmoid ? g * chosen * (1.0f - chosen) : g;
+    if (id >= 0) full[slot][id] = a.sigmoid ? g * chosen * sigmoid(-x) : g;       // 1 - s(x) = s(-x), without cancelling
     wave_sync();
     float d[NV];
 #pragma unroll
