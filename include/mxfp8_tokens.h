@@ -45,10 +45,13 @@ typedef enum { MXFP8_SCORE_SOFTMAX = 0, MXFP8_SCORE_SIGMOID = 1 } mxfp8_score;
  * Equal values go to the lower index, for experts and for runs.  The choice
  * is that of scores held in fp64 (scores closer than fp32 can tell apart are
  * compared again in fp64); without a bias (and with group_top 1, if there are
- * groups) it is that of the logits, which the scores rise with.  A logit of -Inf has score 0; if softmax has no
- * logit above -Inf, or a renormalized sum is 0, the weights are NaN.  With a
- * NaN among the logits the ids are k distinct experts and the weights NaN
- * (sigmoid: those of the NaN experts, all if renormalized).
+ * groups) it is that of the logits, which the scores rise with.
+ *
+ * A logit of -Inf has score 0.  Renormalized weights hold however small the
+ * chosen scores are; they are NaN if no chosen logit is above -Inf, and all
+ * softmax weights are if no logit is, or if one is +Inf.  With a NaN among the
+ * logits the ids are k distinct experts and the weights NaN (sigmoid: those of
+ * the NaN experts, all if renormalized).
  *
  *   logits : [T][E] FP32 or BF16, rows ld >= E elements apart
  *   bias   : FP32 [E] or NULL

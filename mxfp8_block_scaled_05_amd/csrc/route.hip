@@ -70,6 +70,27 @@ __device__ __forceinline__ float fast_sigmoid(float x) {
     return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(x * -kLog2E));
 }
 
+// Chosen scores of a token over e^(their largest logit), one a lane, and their
+// sum.  Renormalized weights are taken from these where the sum of the scores
+// themselves is below kSmallSum: far below, fp32 has no numbers for the scores,
+// though for their quotients, and a softmax score is off by 2^-24 of its
+// distance from the row's largest logit already before.  (The largest score of a
+// softmax is 2^-9 at least, so this is for choices that a bias or groups turn
+// away from it, and for sigmoids of nothing but low logits.)  A sigmoid is
+// e^x s(-x).  NaN if no logit is above -Inf.
+constexpr float kSmallSum = 0x1p-10f;
+struct Shares {
+    float part, sum;
+};
+template <int L>
+__device__ __forceinline__ Shares shares(float x, bool chosen, bool of_sigmoid) {
+    const float most = group_reduce<L>(chosen ? x : -__builtin_inff(), OpMax());
+    Shares r;
+    r.part = chosen ? exp_neg(x - most) * (of_sigmoid ? sigmoid(-x) : 1.0f) : 0.0f;
+    r.sum = group_reduce<L>(r.part, OpAdd());
+    return r;
+}
+
 // The lanes of one token: group (of experts) g, first expert of the lane and
 // how many it holds.
 struct LaneExperts {
@@ -385,7 +406,15 @@ __global__ __launch_bounds__(kBlock, 4) void route_kernel(const RouteArgs a) {
 
     float w = 0.0f;
     if (l < a.k) w = a.sigmoid ? sigmoid(x) : exp_neg(x - top) * inv;
-    if (a.renorm) w = w / group_reduce<L>(w, OpAdd());
+    if (a.renorm) {
+        float sum = group_reduce<L>(w, OpAdd());
+        if (__ballot(sum < kSmallSum)) {
+            const Shares r = shares<L>(x, l < a.k, a.sigmoid);
+            w = sum < kSmallSum ? r.part : w;
+            sum = sum < kSmallSum ? r.sum : sum;
+        }
+        w = w / sum;
+    }
     if (live && l < a.k) {
         a.ids[token * a.k + l] = id;
         a.w[token * a.k + l] = w * a.scale;
@@ -445,17 +474,29 @@ __global__ __launch_bounds__(kBlock) void route_backward_kernel(const RouteArgs 
     if (id >= 0) chosen = a.sigmoid ? sigmoid(x) : exp_neg(x - top) * inv;
     else g = 0.0f;
     float ga = group_reduce<L>(g * chosen, OpAdd());
+    float slope = chosen * (a.sigmoid ? sigmoid(-x) : 1.0f);         // ds / dx: 1 - s(x) = s(-x), without cancelling
+    bool small = false;
     if (a.renorm) {
         const float A = group_reduce<L>(chosen, OpAdd());
+        small = A < kSmallSum;
+        float direct = 0.0f, mean = 0.0f;
+        if (__ballot(small)) {                                       // dx = w (g - sum(g w)), times s(-x)
+            const Shares r = shares<L>(x, id >= 0, a.sigmoid);
+            const float w = id >= 0 ? r.part / r.sum : 0.0f;
+            mean = group_reduce<L>(g * w, OpAdd());
+            direct = w * (a.sigmoid ? sigmoid(-x) : 1.0f) * (g - mean);
+        }
         g = (g - ga / A) / A;
         ga = group_reduce<L>(id >= 0 ? g * chosen : 0.0f, OpAdd());
+        if (small) g = direct, slope = 1.0f, ga = mean - mean;
     }
+    const bool whole = a.sigmoid || small;                           // the chosen experts' gradients are all there is
     wave_sync();
-    if (id >= 0) full[slot][id] = a.sigmoid ? g * chosen * sigmoid(-x) : g;       // 1 - s(x) = s(-x), without cancelling
+    if (id >= 0) full[slot][id] = whole ? g * slope : g;
     wave_sync();
     float d[NV];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) d[i] = a.sigmoid ? mine[i] : s[i] * inv * (mine[i] - ga);
+    for (int i = 0; i < NV; ++i) d[i] = a.sigmoid ? mine[i] : small ? mine[i] + ga : s[i] * inv * (mine[i] - ga);
     if (!live) return;
     E *out = static_cast<E *>(a.dx) + token * a.E + first;
     if constexpr (NV >= Elem<E>::kVec) {
