@@ -37,6 +37,10 @@ def tokens_lib():
     return L
 
 
+# limits of include/mxfp8_tokens.h that have to hold before outputs are allocated
+MAX_K, MAX_EXPERTS, MAX_PAD, MAX_TOP = 32, 1024, 1024, 64
+ERR_SHAPE = 2
+
 _CODES = {torch.float32: MXFP8_F32, torch.bfloat16: MXFP8_BF16}
 
 # The checks below look at the usual tensor first and leave what is not one to

@@ -11,7 +11,7 @@ from dataclasses import dataclass
 import torch
 
 from . import _check
-from ._tokens import need, need_rows, same_device, stream_of, tokens_lib
+from ._tokens import ERR_SHAPE, MAX_TOP, need, need_rows, same_device, stream_of, tokens_lib
 
 
 @dataclass
@@ -45,6 +45,8 @@ def token_logprobs(logits: torch.Tensor, targets: torch.Tensor, *, temperature: 
     stats = logprobs.new_empty(T, 2)
     top = ids = None
     if top_n:
+        if not 0 < top_n <= MAX_TOP:
+            _check(ERR_SHAPE, "mxfp8_token_logprobs")
         top = logprobs.new_empty(T, top_n)
         ids = targets.new_empty(T, top_n)
     need_ws = L.mxfp8_token_logprobs_workspace_bytes(T, V, top_n)

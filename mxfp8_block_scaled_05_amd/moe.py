@@ -14,7 +14,7 @@ from dataclasses import dataclass
 import torch
 
 from . import _check
-from ._tokens import need, need_rows, same_device, stream_of, tokens_lib
+from ._tokens import ERR_SHAPE, MAX_EXPERTS, MAX_K, MAX_PAD, need, need_rows, same_device, stream_of, tokens_lib
 
 _SCORES = {"softmax": 0, "sigmoid": 1}
 
@@ -48,6 +48,8 @@ def route(logits: torch.Tensor, k: int, *, score: str = "softmax", bias: torch.T
             raise ValueError("bias must have E = %d entries" % E)
     dev = same_device(logits, bias)
     sc = _score_code(score)
+    if not 0 < k <= MAX_K:
+        _check(ERR_SHAPE, "mxfp8_route")
     ids = logits.new_empty((T, k), dtype=torch.int32)
     weights = torch.empty_like(ids, dtype=torch.float32)
     _check(tokens_lib().mxfp8_route(logits.data_ptr(), code, ld, T, E, k, sc, b, groups, groups_kept, group_top,
@@ -97,6 +99,8 @@ def route_tables(ids: torch.Tensor, experts: int, pad: int = 32, rows: int | Non
         raise ValueError("ids must be [T, k]")
     T, k = ids.shape
     L = tokens_lib()
+    if not 0 < experts <= MAX_EXPERTS or not 0 < pad <= MAX_PAD or (rows is not None and not 0 <= rows < 1 << 31):
+        _check(ERR_SHAPE, "mxfp8_route_tables")
     if rows is None:
         rows = int(L.mxfp8_route_rows(T * k, experts, pad))
     if T == 0:
