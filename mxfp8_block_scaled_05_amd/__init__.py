@@ -147,10 +147,14 @@ def _ptr(t: torch.Tensor):
     return ctypes.c_void_p(t.data_ptr())
 
 
+# device index -> handle of its current stream: without the Stream object around it where torch has that (0.1 us
+# against 2)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
+
+
 def _stream(device: torch.device):
-    # the handle of torch.cuda.current_stream(device) without the Stream object around it (0.1 us against 2)
     index = device.index
-    return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if index is None else index))
+    return ctypes.c_void_p(_raw_stream(torch.cuda.current_device() if index is None else index))
 
 
 def _need(t: torch.Tensor, dtype, name: str):

@@ -6,7 +6,7 @@ import ctypes
 
 import torch
 
-from . import MXFP8_BF16, MXFP8_F32, _need, lib
+from . import MXFP8_BF16, MXFP8_F32, _need, _raw_stream as stream_of, lib  # noqa: F401
 
 _ready = None
 
@@ -87,6 +87,3 @@ def same_device(first, *others) -> int:
         if t is not None and t.get_device() != d:
             raise ValueError("all tensors must be on one device, got %s and %s" % (first.device, t.device))
     return d
-
-
-stream_of = torch._C._cuda_getCurrentRawStream      # device index -> handle of its current stream
