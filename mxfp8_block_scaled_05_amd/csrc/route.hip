@@ -387,6 +387,7 @@ __global__ __launch_bounds__(kBlock, 4) void route_kernel(const RouteArgs a) {
         const bool whole = count == a.candidates || first_lane<L>(ends, seg) < L;
         const Fp64Row r = fp64_row<L, E>(a, row, ex, top);
         if (__ballot(!whole && live)) {
+            wave_sync();
             choose_fp64<L, NV, E>(a, row, ex, r, keep, lane, sel[slot]);
         } else {
             uint64_t value = order_key(fp64_value(a, r, x, id));

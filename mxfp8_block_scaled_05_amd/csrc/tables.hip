@@ -176,9 +176,9 @@ __global__ __launch_bounds__(kThreads) void route_place_kernel(const RouteTables
         const int rank = __builtin_popcountll(lower);
         int row = -1;
         if (real) row = at[wave][id] + rank;
-        __builtin_amdgcn_wave_barrier();
+        wave_sync();
         if (real && (same >> lane) == 1ull) at[wave][id] = row + 1;   // highest lane of its expert
-        __builtin_amdgcn_wave_barrier();
+        wave_sync();
         if (p < whi) {
             a.pair_row[p] = row;
             if (real) a.row_token[row] = (uint32_t)p / (uint32_t)a.k;
