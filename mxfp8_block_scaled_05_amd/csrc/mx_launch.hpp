@@ -189,8 +189,8 @@ struct RouteArgs {
 hipError_t launch_route(const RouteArgs &a, bool bf16, hipStream_t stream);
 hipError_t launch_route_backward(const RouteArgs &a, bool bf16, hipStream_t stream);
 
-// Row tables (tables.hip).  pairs >= 1; hist: chunks * E ints when a batch
-// takes more than one chunk (route_tables_workspace).
+// Row tables (tables.hip).  pairs >= 1; hist: chunks * E ints where a counting
+// launch comes first (route_tables_workspace_bytes is not 0).
 constexpr int kTablesMaxExperts = 1024;
 constexpr int kTablesMaxChunks = 64;
 struct RouteTables {

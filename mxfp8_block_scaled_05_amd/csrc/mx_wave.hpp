@@ -1,4 +1,4 @@
-// Wavefront building blocks of the routing and token log-probability kernels:
+// Wavefront building blocks of the token-level kernels:
 // reductions over aligned groups of lanes, vector loads of any alignment,
 // order-preserving integer keys, and exponentials.
 #pragma once

@@ -1,6 +1,5 @@
-// Expert routing: the choice of every token's experts and their weights, the
-// gradient of those weights, and the padded, expert-sorted row tables that
-// the gather quantizers and grouped GEMMs read.
+// Expert routing: the choice of every token's experts and their weights, and
+// the gradient of those weights.
 #include "mx_launch.hpp"
 #include "mx_wave.hpp"
 
@@ -22,19 +21,6 @@ __device__ __forceinline__ void load_values(const E *p, int count, float pad, fl
         }
     }
     load_head<NV>(p, count, pad, x);
-}
-
-// Reduction over aligned groups of 2^shift lanes, shift known at run time
-// (the same in all lanes).
-template <class T, class Op>
-__device__ __forceinline__ T reduce_shift(T v, int shift, Op op) {
-    if (shift > 0) v = op(v, partner<0>(v));
-    if (shift > 1) v = op(v, partner<1>(v));
-    if (shift > 2) v = op(v, partner<2>(v));
-    if (shift > 3) v = op(v, partner<3>(v));
-    if (shift > 4) v = op(v, partner<4>(v));
-    if (shift > 5) v = op(v, partner<5>(v));
-    return v;
 }
 
 __device__ __forceinline__ uint64_t shfl64(uint64_t v, int lane) {
