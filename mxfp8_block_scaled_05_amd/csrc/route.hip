@@ -301,9 +301,11 @@ __global__ __launch_bounds__(kBlock, 4) void route_kernel(const RouteArgs a) {
         const bool in = keep;
         keep = keep && rank < a.kept;
         if (!a.order_x) {
-            const float low = group_reduce<L>(keep ? score : __builtin_inff(), OpMin());
-            const float high = group_reduce<L>(in && !keep ? score : kNone, OpMax());
-            const bool close = !(low - high > 2.0f * margin + kRel * (__builtin_fabsf(low) + __builtin_fabsf(high)));
+            // what a group's score may be off by goes by its terms, which can be far larger than their sum
+            const float off = margin + kRel * (__builtin_fabsf(b1) + (a.group_top == 2 ? __builtin_fabsf(b2) : 0.0f));
+            const float low = group_reduce<L>(keep ? score - off : __builtin_inff(), OpMin());
+            const float high = group_reduce<L>(in && !keep ? score + off : kNone, OpMax());
+            const bool close = !(low > high);
             if (__ballot(close && live)) {
                 const float bar = a.group_top == 2 ? b2 : b1;
                 keep = keep_fp64<L, NV, E>(a, row, ex, fp64_row<L, E>(a, row, ex, top), v,
