@@ -266,8 +266,8 @@ __device__ __forceinline__ uint64_t *part_keys(const LogprobsArgs &a) {
 
 // One pass over a slice of a row: running maximum, sum and weighted sum per
 // lane, joined over the block.  2048 rows of 131072 bf16 take 88 us, 6.1 TB/s
-// (a large copy moves 5.3): HBM and the vector ALU (9.2 instructions a logit, busy
-// for 94% of the time) are both at their limits; one row of 131072 5.1 us.
+// (only reading them 80): HBM and the vector ALU (9.2 instructions a logit, busy
+// nearly all of the time) are both at their limits; one row of 131072 5.1 us.
 // ONCE: the logits are larger than the last-level cache and are read past it
 // (91.5 us if not; the call and its gradient 263 us instead of 293).
 //
@@ -427,8 +427,8 @@ __device__ __forceinline__ Line far_line(const LogprobsArgs &a, float m, float l
 // d logits = (g (1[target] - p) - h p (log p + H)) / temp with g, h the
 // gradients of log-probability and entropy, log p = x / temp - m - log_sum.
 // One read and one write of the logits; in place is fine (a thread writes
-// what it alone has read).  2048 rows of 131072 bf16 take 174 us, 6.2 TB/s,
-// more than a large copy's 5.3.  ONCE: what is read and written (in place: the
+// what it alone has read).  2048 rows of 131072 bf16 take 174 us, 6.2 TB/s (a
+// copy past the caches 165).  ONCE: what is read and written (in place: the
 // logits alone) is larger than the last-level cache and goes past it (187 us
 // if not; but 511 rows of 100003 fp32 written, scored and overwritten in place,
 // which fit, would take 185 us instead of 167).  A row of 9000 in two blocks of equal length 53
