@@ -269,7 +269,7 @@ mxfp8_status mxfp8_token_logprobs_backward(const void *logits, mxfp8_dtype dtype
     if (T == 0) return MXFP8_OK;
     if (!logits || !targets || !stats || !d_logits || (!d_logprobs && !d_entropy) || (d_entropy && !entropy))
         return MXFP8_ERR_NULL;
-    if (logits == d_logits && ld != ld_out) return MXFP8_ERR_SHAPE;
+    if (logits == d_logits && ld != ld_out && T > 1) return MXFP8_ERR_SHAPE;
     const size_t e = elem_bytes(dtype);
     if (!aligned(logits, e) || !aligned(d_logits, e) || !aligned(targets, 8) || !aligned(stats, 4) ||
         !aligned(entropy, 4) || !aligned(d_logprobs, 4) || !aligned(d_entropy, 4))
