@@ -49,7 +49,8 @@ typedef enum {
     MXFP8_ERR_HIP = 6,         /* a HIP launch or query failed                        */
     MXFP8_ERR_UNSUPPORTED = 7, /* the current device is not gfx950                    */
     MXFP8_ERR_OVERLAP = 8      /* an output overlaps another buffer of the call
-                                  (checked by the calls of mxfp8_tokens.h)           */
+                                  (checked by the calls of mxfp8_tokens.h and
+                                  mxfp8_policy.h)                                    */
 } mxfp8_status;
 
 typedef enum { MXFP8_F32 = 0, MXFP8_BF16 = 1 } mxfp8_dtype;
@@ -750,5 +751,7 @@ const char *mxfp8_version(void);
 
 /* routing, expert rows and token log-probabilities */
 #include "mxfp8_tokens.h"
+/* activation checkpoints, low-rank adapters, drafted tokens */
+#include "mxfp8_policy.h"
 
 #endif /* MXFP8_H */

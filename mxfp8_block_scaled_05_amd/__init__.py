@@ -943,3 +943,10 @@ from .moe import (RouteTables, moe_combine, moe_combine_backward, route, route_b
 
 __all__ += ["route", "route_backward", "route_rows", "route_tables", "RouteTables", "moe_combine",
             "moe_combine_backward", "token_logprobs", "token_logprobs_backward", "TokenLogprobs"]
+
+
+# ------------------------------------------------------------------ checkpoints, adapters, drafts
+
+from .checkpoint import Swiglu, swiglu, swiglu_backward  # noqa: E402
+
+__all__ += ["swiglu", "swiglu_backward", "Swiglu"]

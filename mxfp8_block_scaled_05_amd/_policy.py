@@ -1,0 +1,36 @@
+"""Signatures and argument checks shared by the calls of
+include/mxfp8_policy.h."""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from . import lib
+from ._tokens import ERR_SHAPE, need, need_rows, same_device, stream_of  # noqa: F401
+
+_ready = None
+
+
+def policy_lib():
+    """The library with these calls' signatures set."""
+    global _ready
+    if _ready is not None:
+        return _ready
+    L = lib()
+    P, I64, I32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int
+    for name, args, res in (
+            ("mxfp8_swiglu", [P, I64, I64, I64, P, P, P, I32, P, P, P], I32),
+            ("mxfp8_swiglu_backward", [P, I64, I64, I64, P, P, P, P, P], I32)):
+        f = getattr(L, name)
+        f.argtypes, f.restype = args, res
+    _ready = L
+    return L
+
+
+def need_bf16_rows(t, name: str) -> int:
+    """The row stride of a 2-D bf16 device tensor whose rows are contiguous."""
+    code, ld = need_rows(t, name)
+    if t.dtype is not torch.bfloat16:
+        raise TypeError("%s must be torch.bfloat16, got %s" % (name, t.dtype))
+    return ld

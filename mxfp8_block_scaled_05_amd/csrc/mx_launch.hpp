@@ -247,6 +247,19 @@ int64_t logprobs_workspace_bytes(int64_t T, int64_t V, int top, int cus);
 hipError_t launch_logprobs(LogprobsArgs a, bool bf16, size_t workspace_bytes, hipStream_t stream);
 hipError_t launch_logprobs_backward(LogprobsArgs a, bool bf16, hipStream_t stream);
 
+// Gated activation with an 8-bit checkpoint (swiglu.hip).  T >= 1.
+struct SwigluArgs {
+    const uint16_t *x;          // gu [T][ld], or d_h [T][ld] (backward)
+    int64_t ld, T;
+    int I;
+    uint16_t *h;                // [T][I] or null
+    uint8_t *hq, *hs;           // h's grid, or null
+    uint8_t *q, *s;             // the checkpoint [T][2 I], [T][2 I / 32] (forward: or null)
+    uint16_t *dx;               // d_gu [T][2 I], backward only
+};
+hipError_t launch_swiglu(const SwigluArgs &a, bool h_packed, hipStream_t stream);
+hipError_t launch_swiglu_backward(const SwigluArgs &a, hipStream_t stream);
+
 // Packed weight layout geometry (see mxfp8_repack in include/mxfp8.h).
 constexpr int64_t kPanelRows = 256;   // rows per packed panel
 constexpr int64_t kKStep = 128;       // K bytes per packed k-step (one MFMA K)
