@@ -1,7 +1,8 @@
 /*
  * mxfp8_policy.h -- C ABI of the operators that a policy trained and sampled
  * with low-rank adapters needs around the MXFP8 layers: the gated activation
- * with its inputs kept in 8 bits for the backward pass.
+ * with its inputs kept in 8 bits for the backward pass, and the adapters
+ * beside a shared projection with their gradients.
  *
  * The conventions of mxfp8.h hold (row-major, caller-owned buffers, host
  * validation before anything is enqueued, one stream, no allocation, no
@@ -58,6 +59,82 @@ mxfp8_status mxfp8_swiglu(const void *gu_bf16, int64_t ld, int64_t T, int64_t I,
  */
 mxfp8_status mxfp8_swiglu_backward(const void *d_h_bf16, int64_t ld, int64_t T, int64_t I, const uint8_t *saved_q,
                                    const uint8_t *saved_s, void *d_gu_bf16, void *h_bf16, hipStream_t stream);
+
+/*
+ * Low-rank adapters of many requests beside a shared projection.
+ *
+ * Row t of a batch belongs to adapter e (or to none); adapter e adds
+ *   scales[e] * B_e (A_e x_t)
+ * to the shared projection's output y_t.  The rows come through the row tables
+ * of mxfp8_route_tables, built with k = 1, the adapters as experts and pad a
+ * multiple of 32 (once for all the layers of a batch):
+ *   offsets   : DEVICE int32 [E+1], every entry a multiple of 32
+ *   row_token : DEVICE int64 [rows], rows % 32 == 0: the row t of each sorted
+ *               row, outside [0, T) for padding (it then adds nothing); rows
+ *               from offsets[E] on are padding whatever they hold
+ * Entries of offsets are clamped to [0, rows]; a row t named twice gets one of
+ * its sums.  Malformed tables can give wrong sums, never an access outside the
+ * buffers.
+ *
+ *   x : BF16 [T][K], rows ld_x elements apart
+ *   a : BF16 [E][r][K];  b : BF16 [E][N][r];  scales : FP32 [E] or NULL (all 1)
+ *   hidden : FP32 [rows][r], A_e x_t of every sorted row (zeros in padding)
+ *
+ * Common limits: 1 <= E <= 1024, 8 <= r <= 128 and r % 8 == 0 (pad a smaller
+ * rank with zeros), K, N >= 8, K % 8 == 0, N % 8 == 0, strides % 8 == 0, 0 <=
+ * T < 2^31, 0 <= rows < 2^31, T * stride <= 2^60, rows / 32 * ceil(max(K,
+ * N) / 256) < 2^24, (rows / 256 + E) * ceil((K + N) / 128) < 2^22, E * r * (K +
+ * N) < 2^40; all pointers 16-byte aligned but offsets and scales (4) and row_token (8).  T = 0: every row is padding.
+ * The adapters' sums are held in fp32; A x enters the second product as two
+ * BF16 numbers that together keep 16 bits of it.
+ */
+
+/* Workspace bytes of mxfp8_lora_add (0 for invalid sizes). */
+size_t mxfp8_lora_add_workspace_bytes(int64_t rows, int64_t E, int64_t r, int64_t K, int64_t N);
+
+/*
+ * mxfp8_lora_add -- y += the adapters' products, in place.
+ *   y : [T][N] FP32 or BF16, rows ld_y >= N elements apart; rows without an
+ *       adapter are neither read nor written
+ *   hidden : or NULL; kept for mxfp8_lora_backward
+ *   workspace : mxfp8_lora_add_workspace_bytes(..) bytes, 16-byte aligned
+ */
+mxfp8_status mxfp8_lora_add(void *y, mxfp8_dtype y_dtype, int64_t ld_y, const void *x_bf16, int64_t ld_x, int64_t T,
+                            const void *a_bf16, const void *b_bf16, const float *scales, int64_t E, int64_t r,
+                            int64_t K, int64_t N, const int32_t *offsets, const int64_t *row_token, int64_t rows,
+                            float *hidden, void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* The forms of mxfp8_lora_backward's x. */
+typedef enum { MXFP8_INPUT_BF16 = 0, MXFP8_INPUT_CANONICAL = 1, MXFP8_INPUT_PACKED = 2 } mxfp8_input;
+
+/* Workspace bytes of mxfp8_lora_backward (0 for invalid sizes). */
+size_t mxfp8_lora_backward_workspace_bytes(int64_t rows, int64_t E, int64_t r, int64_t K, int64_t N);
+
+/*
+ * mxfp8_lora_backward -- gradients of mxfp8_lora_add.
+ *
+ *   S_t  = scales[e] * B_e^T d_y_t
+ *   d_x += A_e^T S_t, in place: BF16 [T][K], rows ld_dx apart, the gradient
+ *          that the shared projection's own product wrote before; NULL: left out
+ *   d_a  = sum_t S_t x_t^T : FP32 [E][r][K];  d_b = sum_t scales[e] d_y_t
+ *          hidden_t^T : FP32 [E][N][r]; all of both is written, zeros for an
+ *          adapter without rows
+ *   d_y : BF16 [T][N], rows ld_dy apart;  hidden as mxfp8_lora_add gave it
+ *   x   : MXFP8_INPUT_BF16: BF16 [T][K], rows ld_x apart, x_s NULL
+ *         MXFP8_INPUT_CANONICAL: mxfp8_quantize(x, axis 1)'s grid in x and x_s
+ *           (K % 32 == 0; ld_x is not read): the input kept in 8 bits
+ *         MXFP8_INPUT_PACKED: the same in mxfp8_repack's layout (N = T), the
+ *           operand that the shared projection itself read
+ *   workspace : mxfp8_lora_backward_workspace_bytes(..) bytes, 16-byte aligned
+ * The sums over rows are cut at places that follow from the sizes alone and
+ * joined in order.
+ */
+mxfp8_status mxfp8_lora_backward(void *d_x_bf16, int64_t ld_dx, const void *d_y_bf16, int64_t ld_dy, const void *x,
+                                 const uint8_t *x_s, mxfp8_input x_input, int64_t ld_x, int64_t T,
+                                 const void *a_bf16, const void *b_bf16, const float *scales, int64_t E, int64_t r, int64_t K, int64_t N,
+                                 const int32_t *offsets, const int64_t *row_token, int64_t rows, const float *hidden,
+                                 float *d_a, float *d_b, void *workspace, size_t workspace_bytes,
+                                 hipStream_t stream);
 
 #ifdef __cplusplus
 }

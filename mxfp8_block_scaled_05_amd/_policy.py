@@ -18,10 +18,15 @@ def policy_lib():
     if _ready is not None:
         return _ready
     L = lib()
-    P, I64, I32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int
+    P, I64, I32, SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t
     for name, args, res in (
             ("mxfp8_swiglu", [P, I64, I64, I64, P, P, P, I32, P, P, P], I32),
-            ("mxfp8_swiglu_backward", [P, I64, I64, I64, P, P, P, P, P], I32)):
+            ("mxfp8_swiglu_backward", [P, I64, I64, I64, P, P, P, P, P], I32),
+            ("mxfp8_lora_add_workspace_bytes", [I64] * 5, SZ),
+            ("mxfp8_lora_add", [P, I32, I64, P, I64, I64, P, P, P, I64, I64, I64, I64, P, P, I64, P, P, SZ, P], I32),
+            ("mxfp8_lora_backward_workspace_bytes", [I64] * 5, SZ),
+            ("mxfp8_lora_backward", [P, I64, P, I64, P, P, I32, I64, I64, P, P, P, I64, I64, I64, I64, P, P, I64, P, P,
+                                     P, P, SZ, P], I32)):
         f = getattr(L, name)
         f.argtypes, f.restype = args, res
     _ready = L

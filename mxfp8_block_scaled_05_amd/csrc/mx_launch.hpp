@@ -260,6 +260,74 @@ struct SwigluArgs {
 hipError_t launch_swiglu(const SwigluArgs &a, bool h_packed, hipStream_t stream);
 hipError_t launch_swiglu_backward(const SwigluArgs &a, hipStream_t stream);
 
+// Low-rank adapters (lora.hip).  rows: sorted rows, a multiple of 32.
+constexpr int kLoraMaxRank = 128;
+constexpr int kLoraMaxAdapters = 1024;
+struct LoraShrink {
+    const uint16_t *x;          // [T][ld], K columns
+    int64_t ld, T;
+    const uint16_t *w;          // [E][r][K]
+    const int32_t *offsets;     // [E + 1]
+    const int64_t *row_token;   // [rows]
+    int64_t rows;
+    float *part;                // [splits][rows][r]
+    int E, r, K, splits, slice;
+};
+struct LoraCut {
+    int splits, slice;
+};
+LoraCut lora_cut(int64_t rows, int64_t K, int cus);
+hipError_t launch_lora_shrink(const LoraShrink &a, hipStream_t stream);
+struct LoraExpand {
+    void *y;                    // [T][ld], N columns
+    int64_t ld, T;
+    const uint16_t *w;          // [E][N][r]
+    const float *scales;        // [E] or null
+    const int32_t *offsets;
+    const int64_t *row_token;
+    int64_t rows;
+    const float *part;          // [splits][rows][r]
+    float *hidden;              // [rows][r] or null: the sum of the partials
+    int E, r, N, splits;
+    int tiles;                  // set by the launcher
+};
+hipError_t launch_lora_expand(LoraExpand a, bool y_bf16, hipStream_t stream);
+struct LoraTranspose {
+    struct Job {
+        const uint16_t *from;   // [E][P][Q]
+        uint16_t *to;           // [E][Q][P]
+        int P, Q;
+    } job[2];
+    int E;
+};
+hipError_t launch_lora_transpose(const LoraTranspose &a, hipStream_t stream);
+// sums over rows, cut into chunks: items at most, slots of partial sums at most
+struct LoraOuterPlan {
+    int64_t chunk, items, slots;
+};
+LoraOuterPlan lora_outer_plan(int64_t rows, int64_t E, int64_t r, int64_t K, int64_t N, int cus);
+struct LoraWide {
+    const float *p;             // [rows][r]
+    const void *x;              // [T][ld] bf16, or a grid's codes
+    const uint8_t *s;           // the grid's scales
+    int64_t ld, ksteps;
+    int C;                      // columns
+    float *out;                 // [E][r][C] (the first) or [E][C][r] (the second)
+    float *part;                // slots of the same
+    int slabs;                  // set by the launcher
+};
+struct LoraOuter {
+    LoraWide wide[2];           // the second is bf16
+    const float *scales;
+    const int32_t *offsets;
+    const int64_t *row_token;
+    int64_t rows, T;
+    int E, r;
+    int chunk, slots, passes;   // set by the launcher
+};
+// form of the first wide matrix: 0 bf16, 1 canonical grid, 2 packed
+hipError_t launch_lora_outer(LoraOuter a, const LoraOuterPlan &plan, int form, hipStream_t stream);
+
 // Packed weight layout geometry (see mxfp8_repack in include/mxfp8.h).
 constexpr int64_t kPanelRows = 256;   // rows per packed panel
 constexpr int64_t kKStep = 128;       // K bytes per packed k-step (one MFMA K)
