@@ -85,8 +85,9 @@ mxfp8_status mxfp8_swiglu_backward(const void *d_h_bf16, int64_t ld, int64_t T, 
  * T < 2^31, 0 <= rows < 2^31, T * stride <= 2^60, rows / 32 * ceil(max(K,
  * N) / 256) < 2^24, (rows / 256 + E) * ceil((K + N) / 128) < 2^22, E * r * (K +
  * N) < 2^40; all pointers 16-byte aligned but offsets and scales (4) and row_token (8).  T = 0: every row is padding.
- * The adapters' sums are held in fp32; A x enters the second product as two
- * BF16 numbers that together keep 16 bits of it.
+ * The adapters' sums are held in fp32; A x and S enter the next product as sums
+ * of BF16 numbers that keep all 24 bits where the result is FP32, 16 where it
+ * is BF16.
  */
 
 /* Workspace bytes of mxfp8_lora_add (0 for invalid sizes). */

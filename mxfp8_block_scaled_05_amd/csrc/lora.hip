@@ -14,10 +14,13 @@
 // shrink (d_y, B^T), expand (d_x, A^T), outer twice (d_a: S and x; d_b: hidden
 // and d_y).
 //
-// P is held in fp32.  Where it is an operand of the matrix unit it enters as
-// two bf16 numbers, hi + lo, which keep 16 bits of it (2^-16 of the value lost;
-// a single one would lose 2^-8, more than bf16 inputs allow the fp32 gradients
-// of the weights).  The second product costs matrix time that is idle anyway.
+// P is held in fp32.  Where it is an operand of the matrix unit it enters as a
+// sum of bf16 numbers: three, which hold all 24 bits, where the result is fp32
+// (y, the weights' gradients), two, which lose 2^-16 of the value, where it is
+// rounded to bf16 (2^-8).  The products of the parts cost matrix time that is
+// idle anyway: these kernels wait for memory.
+#include <type_traits>
+
 #include "mx_launch.hpp"
 #include "mx_wave.hpp"
 
@@ -33,15 +36,21 @@ __device__ __forceinline__ v4f mfma(v4u a, v4u b, v4f c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, a), __builtin_bit_cast(v8bf, b), c, 0, 0, 0);
 }
 
-// Two values as hi + lo, each pair of bf16 in a word.  What the rounding to bf16
-// takes to infinity, or was infinite, has no rest.
-__device__ __forceinline__ float rest_of(float v, float hi) {
-    const float d = v - hi;
+// Two values as a sum of N pairs of bf16, each pair in a word, the largest
+// first.  What the rounding to bf16 takes to infinity, or was infinite, has no
+// rest.
+__device__ __forceinline__ float rest_of(float v, float taken) {
+    const float d = v - taken;
     return d == d ? d : 0.0f;
 }
-__device__ __forceinline__ void split2(float v0, float v1, uint32_t &hi, uint32_t &lo) {
-    hi = bf16x2_rne(v0, v1);
-    lo = bf16x2_rne(rest_of(v0, __uint_as_float(hi << 16)), rest_of(v1, __uint_as_float(hi & 0xFFFF0000u)));
+template <int N>
+__device__ __forceinline__ void split_pair(float v0, float v1, uint32_t (&out)[N]) {
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        out[n] = bf16x2_rne(v0, v1);
+        v0 = rest_of(v0, __uint_as_float(out[n] << 16));
+        v1 = rest_of(v1, __uint_as_float(out[n] & 0xFFFF0000u));
+    }
 }
 
 // The number of offsets[0..E] that are at most row, less one: the group that
@@ -65,67 +74,118 @@ __device__ __forceinline__ int token_of(const int64_t *row_token, int64_t row, i
 // ---------------------------------------------------------------- shrink
 
 // One block: 32 sorted rows, a slice of the wide axis, all ranks.  Its waves
-// take chunks of 128 columns in turn.  RT: tiles of 16 ranks.
+// take chunks of it in turn, each on its own.  RT: tiles of 16 ranks.
+//
+// The matrix unit wants 16 rows from 16 neighbouring lanes, and a load that is
+// laid out so touches 16 cache lines with every 256 bytes it brings (8192 rows
+// of 6144: 34 us, 10 bytes a clock from a compute unit's cache).  So both
+// operands are loaded in runs of 256 or 128 bytes of a row, kept in registers
+// until the chunk before is used, and turned in the wave's part of LDS: row r's
+// 16-byte piece c lies at c ^ r, which spreads 16 rows over the banks.
+template <int RT>
+struct ShrinkShape {
+    static constexpr int kChunk = RT <= 2 ? 128 : 64;            // columns of a wave's chunk
+    static constexpr int kPieces = kChunk / 8;                   // 16-byte pieces of a row of it
+    static constexpr int kPass = 64 / kPieces;                   // rows that a wave loads at once
+    static constexpr int kX = kRows / kPass, kW = RT * 16 / kPass;
+    static constexpr int kWaveBytes = (kRows + RT * 16) * kChunk * 2;
+    static constexpr int kRedBytes = kWaves * kRows * RT * 64;
+    static constexpr int kBytes = kWaves * kWaveBytes > kRedBytes ? kWaves * kWaveBytes : kRedBytes;
+};
+
 template <int RT>
 __global__ __launch_bounds__(kBlock) void lora_shrink_kernel(const LoraShrink a) {
-    __shared__ v4f red[kWaves][kRows][RT * 4];
+    using S = ShrinkShape<RT>;
+    __shared__ v4u room[S::kBytes / 16];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int m = lane & 15, kg = lane >> 4;
     const int rb = blockIdx.x / a.splits, split = blockIdx.x - rb * a.splits;
     const int e = adapter_of(a.offsets, a.E, rb * kRows, lane);
     if (e < 0 || e >= a.E) return;                       // the whole block
-    const uint16_t *x[2];
-    bool real[2];
+    // Rows of padding are loaded from row 0 and ranks past r from rank 0: what they give is not kept, and loads that
+    // nothing branches around let the compiler wait for the oldest alone.
+    const int piece = lane % S::kPieces, sub = lane / S::kPieces;
+    const uint16_t *x[S::kX], *w[S::kW];
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-        const int token = token_of(a.row_token, (int64_t)rb * kRows + t * 16 + m, a.T);
-        real[t] = token >= 0;
-        x[t] = a.x + (real[t] ? token : 0) * a.ld;
+    for (int i = 0; i < S::kX; ++i) {
+        const int token = token_of(a.row_token, (int64_t)rb * kRows + i * S::kPass + sub, a.T);
+        x[i] = a.x + (token < 0 ? 0 : token) * a.ld + piece * 8;
     }
-    const bool second = __ballot(real[1]) != 0;
-    const uint16_t *w[RT];
-    bool rank[RT];
 #pragma unroll
-    for (int j = 0; j < RT; ++j) {
-        rank[j] = j * 16 + m < a.r;
-        w[j] = a.w + ((int64_t)e * a.r + (rank[j] ? j * 16 + m : 0)) * a.K;
+    for (int i = 0; i < S::kW; ++i) {
+        const int rank = i * S::kPass + sub;
+        w[i] = a.w + ((int64_t)e * a.r + (rank < a.r ? rank : 0)) * a.K + piece * 8;
     }
     v4f acc[2][RT];
 #pragma unroll
     for (int t = 0; t < 2; ++t)
 #pragma unroll
         for (int j = 0; j < RT; ++j) acc[t][j] = v4f{0, 0, 0, 0};
-    const v4u zero = {0, 0, 0, 0};
+
     const int k1 = min(a.K, (split + 1) * a.slice);
-    for (int k0 = split * a.slice + wave * 128; k0 < k1; k0 += kWaves * 128) {
-        v4u xf[4][2], wf[4][RT];
+    v4u xs[S::kX], ws[S::kW];
+    auto ask = [&](int k0) {
 #pragma unroll
-        for (int s = 0; s < 4; ++s) {
-            const int k = k0 + s * 32 + kg * 8;
-            const bool in = k < k1;
-            const int at = in ? k : 0;
+        for (int i = 0; i < S::kX; ++i) xs[i] = *reinterpret_cast<const v4u *>(x[i] + k0);
 #pragma unroll
-            for (int t = 0; t < 2; ++t)
-                if (t == 0 || second) {
-                    const v4u v = *reinterpret_cast<const v4u *>(x[t] + at);
-                    xf[s][t] = in && real[t] ? v : zero;
-                }
+        for (int i = 0; i < S::kW; ++i) ws[i] = *reinterpret_cast<const v4u *>(w[i] + k0);
+    };
+    auto ask_end = [&](int k0) {                         // the columns below k1 and zeros
+        const bool in = k0 + piece * 8 < k1;
+        const int64_t back = in ? k0 : -piece * 8;
 #pragma unroll
-            for (int j = 0; j < RT; ++j) {
-                const v4u v = *reinterpret_cast<const v4u *>(w[j] + at);
-                wf[s][j] = in && rank[j] ? v : zero;
-            }
+        for (int i = 0; i < S::kX; ++i) {
+            const v4u v = *reinterpret_cast<const v4u *>(x[i] + back);
+            xs[i] = in ? v : v4u{0, 0, 0, 0};
         }
 #pragma unroll
-        for (int s = 0; s < 4; ++s)
+        for (int i = 0; i < S::kW; ++i) {
+            const v4u v = *reinterpret_cast<const v4u *>(w[i] + back);
+            ws[i] = in ? v : v4u{0, 0, 0, 0};
+        }
+    };
+    v4u *mine = room + wave * (S::kWaveBytes / 16);
+    auto slot = [&](int row, int c) { return row * S::kPieces + (c ^ (row % S::kPieces)); };
+    auto turn = [&]() {
 #pragma unroll
-            for (int t = 0; t < 2; ++t)
-                if (t == 0 || second) {
+        for (int i = 0; i < S::kX; ++i) mine[slot(i * S::kPass + sub, piece)] = xs[i];
 #pragma unroll
-                    for (int j = 0; j < RT; ++j) acc[t][j] = mfma(wf[s][j], xf[s][t], acc[t][j]);
-                }
+        for (int i = 0; i < S::kW; ++i) mine[slot(kRows + i * S::kPass + sub, piece)] = ws[i];
+        wave_sync();
+    };
+    auto use = [&]() {
+#pragma unroll
+        for (int s = 0; s < S::kChunk / 32; ++s) {
+            v4u wf[RT];
+#pragma unroll
+            for (int j = 0; j < RT; ++j) wf[j] = mine[slot(kRows + j * 16 + m, s * 4 + kg)];
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                const v4u xf = mine[slot(t * 16 + m, s * 4 + kg)];
+#pragma unroll
+                for (int j = 0; j < RT; ++j) acc[t][j] = mfma(wf[j], xf, acc[t][j]);
+            }
+        }
+        wave_sync();
+    };
+    constexpr int kStep = kWaves * S::kChunk;
+    int k0 = split * a.slice + wave * S::kChunk;
+    if (k0 + S::kChunk <= k1) {
+        ask(k0);
+        for (; k0 + S::kChunk <= k1; k0 += kStep) {
+            turn();
+            ask(k0 + kStep + S::kChunk <= k1 ? k0 + kStep : k0);         // the last time for nothing
+            use();
+        }
+    }
+    if (k0 < k1) {
+        ask_end(k0);
+        turn();
+        use();
     }
     // a lane holds four ranks, 4 kg.., of row m
+    __syncthreads();
+    auto red = reinterpret_cast<v4f (*)[kRows][RT * 4]>(room);
 #pragma unroll
     for (int t = 0; t < 2; ++t)
 #pragma unroll
@@ -138,56 +198,51 @@ __global__ __launch_bounds__(kBlock) void lora_shrink_kernel(const LoraShrink a)
         v4f v = red[0][row][q];
 #pragma unroll
         for (int n = 1; n < kWaves; ++n) v += red[n][row][q];
+        if (token_of(a.row_token, (int64_t)rb * kRows + row, a.T) < 0) v = v4f{0, 0, 0, 0};
         *reinterpret_cast<v4f *>(out + (int64_t)row * a.r + q * 4) = v;
     }
 }
 
 // ---------------------------------------------------------------- expand
 
-// 16 consecutive values of a row of y, those below `left` columns (a multiple of 8)
+// y in 16-byte pieces: of a row's 64 columns, those that a wave loads of so
+// many rows at once
 template <class Y>
-struct Run16;
-template <>
-struct Run16<uint16_t> {
-    v4u r[2];
-    __device__ __forceinline__ void load(const uint16_t *p, int left) {
-        if (left > 0) r[0] = *reinterpret_cast<const v4u *>(p);
-        if (left > 8) r[1] = *reinterpret_cast<const v4u *>(p + 8);
-    }
-    __device__ __forceinline__ void add_store(uint16_t *p, int left, const v4f *d) {
-        float f[16];
-        Elem<uint16_t>::unpack(r[0], f), Elem<uint16_t>::unpack(r[1], f + 8);
+struct Tile {
+    static constexpr int kVec = 16 / sizeof(Y), kPieces = 64 / kVec, kPass = 64 / kPieces, kPasses = 16 / kPass;
+    __device__ static __forceinline__ v4u add(v4u y, const float *d) {
+        float f[kVec];
+        Elem<Y>::unpack(y, f);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) f[i] += d[i >> 2][i & 3];
-        if (left > 0) *reinterpret_cast<v4u *>(p) = Elem<uint16_t>::pack(f);
-        if (left > 8) *reinterpret_cast<v4u *>(p + 8) = Elem<uint16_t>::pack(f + 8);
-    }
-};
-template <>
-struct Run16<float> {
-    v4f r[4];
-    __device__ __forceinline__ void load(const float *p, int left) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (left > i * 4) r[i] = *reinterpret_cast<const v4f *>(p + i * 4);
-    }
-    __device__ __forceinline__ void add_store(float *p, int left, const v4f *d) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (left > i * 4) *reinterpret_cast<v4f *>(p + i * 4) = r[i] + d[i];
+        for (int i = 0; i < kVec; ++i) f[i] += d[i];
+        return Elem<Y>::pack(f);
     }
 };
 
-// One block: RB groups of 32 sorted rows x 256 columns, a wave 64 of them.  The
-// products are taken as B P^T, with the rows of B that a tile of 16 takes chosen
-// so that a lane ends up with 16 consecutive columns of one row of y.
-// KT: steps of 32 ranks.
-template <class Y, int KT, int RB>
-__global__ __launch_bounds__(kBlock) void lora_expand_kernel(const LoraExpand a) {
-    __shared__ v4u frag[RB * 2][KT][2][64];              // P of each 16 rows as the matrix unit takes it: hi, lo
+// One block: RB groups of 32 sorted rows; its waves go through their columns
+// 64 at a time, `step` apart.  The products of 16 rows are taken as B P^T and
+// turned in the wave's part of LDS, so that y is read and written in runs of
+// 128 or 256 bytes (in the matrix unit's own layout 16 neighbouring lanes hold
+// 16 rows, 16 cache lines for 256 bytes).  The next columns' y and B are asked
+// for before the current ones are used.  Joining P once for many columns
+// matters: 8192 rows of rank 64 to 6144 take 60 us with P joined for every 256.
+// KT: steps of 32 ranks.  LOOP: several columns.
+//
+// B's rows are r long, so 64 of them are one run of memory.  Above rank 32 they
+// are loaded as such and turned in LDS; loaded straight into fragments they
+// would touch a cache line for every 16 bytes (twice the time of y itself).
+template <class Y, int KT, int RB, bool LOOP>
+__global__ __launch_bounds__(kBlock, KT == 4 ? 1 : 2) void lora_expand_kernel(const LoraExpand a) {
+    using T = Tile<Y>;
+    constexpr int kParts = sizeof(Y) == 4 ? 3 : 2, kPasses = T::kPasses;
+    __shared__ v4u frag[RB * 2][KT][kParts][64];         // P of each 16 rows as the matrix unit takes it, in parts
+    __shared__ float turn[kWaves][16][68];               // 4 more than a row: 16 rows on all banks
+    constexpr bool kTurnB = KT > 1;
+    constexpr int kB = 4 * KT;                           // 16-byte pieces of a row of B, and of a lane's B
+    __shared__ v4u bs[kTurnB ? kWaves * 64 * kB : 1];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int m = lane & 15, kg = lane >> 4;
-    const int group = blockIdx.x / a.tiles, tile = blockIdx.x - group * a.tiles;
+    const int group = blockIdx.x / a.step, tile0 = blockIdx.x - group * a.step;
     const int rb0 = group * RB;
     const int blocks = (int)(a.rows / kRows);
     int e[RB];
@@ -196,9 +251,139 @@ __global__ __launch_bounds__(kBlock) void lora_expand_kernel(const LoraExpand a)
         e[i] = rb0 + i < blocks ? adapter_of(a.offsets, a.E, (rb0 + i) * kRows, lane) : -1;
         if (e[i] >= a.E) e[i] = -1;
     }
+    const int piece = lane % T::kPieces, sub = lane / T::kPieces;
+    int token[RB * 2][kPasses];
+#pragma unroll
+    for (int i = 0; i < RB * 2; ++i)
+#pragma unroll
+        for (int p = 0; p < kPasses; ++p)
+            token[i][p] = e[i >> 1] < 0 ? -1 : token_of(a.row_token, (int64_t)rb0 * kRows + i * 16 + p * T::kPass + sub, a.T);
+
+    struct Ahead {
+        v4u y[RB * 2][kPasses];
+        v4u b[kTurnB ? 1 : kB];                          // fragments [q]
+    };
+    v4u run[kTurnB ? kB : 1];                            // or the run's pieces: one set, in LDS before the next is asked for
+    v4u *mine = bs + wave * 64 * kB;
+    auto slot = [&](int n, int c) { return n * kB + (c ^ (n % (kB < 16 ? kB : 16))); };
+    int b_slot[kTurnB ? kB : 1], b_piece[kTurnB ? kB : 1];
+    if constexpr (kTurnB) {
+        const int per = a.r / 8;                         // pieces of a row
+#pragma unroll
+        for (int i = 0; i < kB; ++i) {
+            const int at = i < per ? i * 64 + lane : lane;               // pieces that there are not: the first again
+            b_piece[i] = at;
+            b_slot[i] = slot(at / per, at % per);
+            mine[i * 64 + lane] = v4u{0, 0, 0, 0};       // ranks past r
+        }
+        wave_sync();
+    }
+    // All 64 rows have a token, one adapter and whole columns: nothing is branched around, so that the compiler counts
+    // what is in flight and waits for the oldest alone.  Otherwise rows of padding and columns past N are loaded from
+    // row 0 and column 0 and not stored.
+    bool whole = a.N % 64 == 0;
+#pragma unroll
+    for (int i = 0; i < RB * 2; ++i)
+#pragma unroll
+        for (int p = 0; p < kPasses; ++p) whole = whole && __ballot(token[i][p] >= 0) == ~0ull && e[i >> 1] == e[0];
+    auto place = [&](int i, int p, int c0) {
+        const int col = c0 + piece * T::kVec;
+        return static_cast<Y *>(a.y) + (token[i][p] < 0 ? 0 : token[i][p]) * a.ld + (col < a.N ? col : 0);
+    };
+    auto ask = [&](Ahead &n, int adapter, int c0) {
+        const uint16_t *w = a.w + ((int64_t)adapter * a.N + c0) * a.r;
+        if constexpr (kTurnB) {
+            const int pieces = min(a.N - c0, 64) * (a.r / 8);
+#pragma unroll
+            for (int i = 0; i < kB; ++i) run[i] = *reinterpret_cast<const v4u *>(w + (b_piece[i] < pieces ? b_piece[i] : 0) * 8);
+        } else {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int col = q * 16 + m, j = kg * 8;
+                const v4u v = *reinterpret_cast<const v4u *>(w + (c0 + col < a.N ? col : 0) * a.r + (j < a.r ? j : 0));
+                n.b[q] = j < a.r ? v : v4u{0, 0, 0, 0};
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < RB * 2; ++i)
+#pragma unroll
+            for (int p = 0; p < kPasses; ++p) n.y[i][p] = *reinterpret_cast<const v4u *>(place(i, p, c0));
+    };
+    auto turn_b = [&]() {
+        if constexpr (kTurnB) {
+#pragma unroll
+            for (int i = 0; i < kB; ++i) mine[b_slot[i]] = run[i];
+            wave_sync();
+        }
+    };
+    auto use = [&](auto whole_rows, const Ahead &n, int adapter, int c0) {
+        constexpr bool kWhole = decltype(whole_rows)::value;
+        const bool in = c0 + piece * T::kVec < a.N;
+#pragma unroll
+        for (int i = 0; i < RB * 2; ++i) {
+            if constexpr (!kWhole) {
+                bool any = false;
+#pragma unroll
+                for (int p = 0; p < kPasses; ++p) any = any || __ballot(token[i][p] >= 0) != 0;
+                if (!any || e[i >> 1] != adapter) continue;
+            }
+            v4f d[4] = {v4f{0, 0, 0, 0}, v4f{0, 0, 0, 0}, v4f{0, 0, 0, 0}, v4f{0, 0, 0, 0}};
+#pragma unroll
+            for (int kt = 0; kt < KT; ++kt) {
+                v4u b[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) b[q] = kTurnB ? mine[slot(q * 16 + m, kt * 4 + kg)] : n.b[q];
+#pragma unroll
+                for (int s = kParts - 1; s >= 0; --s) {
+                    const v4u p = frag[i][kt][s][lane];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) d[q] = mfma(b[q], p, d[q]);
+                }
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q) *reinterpret_cast<v4f *>(&turn[wave][m][q * 16 + kg * 4]) = d[q];
+            wave_sync();
+#pragma unroll
+            for (int p = 0; p < kPasses; ++p) {
+                float f[T::kVec];
+#pragma unroll
+                for (int v = 0; v < T::kVec; v += 4) {
+                    const v4f u = *reinterpret_cast<const v4f *>(&turn[wave][p * T::kPass + sub][piece * T::kVec + v]);
+                    f[v] = u.x, f[v + 1] = u.y, f[v + 2] = u.z, f[v + 3] = u.w;
+                }
+                if (kWhole || (in && token[i][p] >= 0)) *reinterpret_cast<v4u *>(place(i, p, c0)) = T::add(n.y[i][p], f);
+            }
+            wave_sync();
+        }
+    };
+    auto columns = [&](auto whole_rows, Ahead (&n)[1 + LOOP], int adapter, int c0, int step) {
+        if constexpr (!LOOP) {
+            if (c0 >= a.N) return;
+            turn_b();
+            use(whole_rows, n[0], adapter, c0);
+        } else {
+            for (; c0 < a.N; c0 += 2 * step) {
+                turn_b();
+                ask(n[1], adapter, c0 + step < a.N ? c0 + step : c0);    // the last time for nothing
+                use(whole_rows, n[0], adapter, c0);
+                if (c0 + step >= a.N) break;
+                turn_b();
+                ask(n[0], adapter, c0 + 2 * step < a.N ? c0 + 2 * step : c0 + step);
+                use(whole_rows, n[1], adapter, c0 + step);
+            }
+        }
+    };
+    const int first = (tile0 * kWaves + wave) * 64, step = a.step * kWaves * 64;
+    int start = 0;                                       // the first group that has an adapter
+#pragma unroll
+    for (int i = RB - 1; i >= 0; --i) start = e[i] >= 0 ? i : start;
+    const int lead = e[start];
+    Ahead ahead[1 + LOOP];
+    if (lead >= 0 && first < a.N) ask(ahead[0], lead, first);
+
     for (int i = threadIdx.x; i < RB * 2 * KT * 64; i += kBlock) {
         const int l = i & 63, kt = (i >> 6) % KT, mt = (i >> 6) / KT;
-        const int ee = RB == 1 ? e[0] : mt < 2 ? e[0] : mt < 4 ? e[RB > 1 ? 1 : 0] : mt < 6 ? e[RB > 2 ? 2 : 0] : e[RB > 3 ? 3 : 0];
+        const int ee = RB == 1 || mt < 2 ? e[0] : e[RB - 1];
         const int64_t row = (int64_t)rb0 * kRows + mt * 16 + (l & 15);
         const int j = kt * 32 + (l >> 4) * 8;
         float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
@@ -211,65 +396,32 @@ __global__ __launch_bounds__(kBlock) void lora_expand_kernel(const LoraExpand a)
                 for (int q = 0; q < 4; ++q) v[q] += lo[q], v[4 + q] += hi[q];
             }
         }
-        if (a.hidden && tile == 0 && in) {
+        if (a.hidden && tile0 == 0 && in) {
             float *h = a.hidden + row * a.r + j;
             *reinterpret_cast<v4f *>(h) = v4f{v[0], v[1], v[2], v[3]};
             *reinterpret_cast<v4f *>(h + 4) = v4f{v[4], v[5], v[6], v[7]};
         }
         const float scale = a.scales && ee >= 0 ? a.scales[ee] : 1.0f;
-        v4u hi, lo;
+        v4u parts[kParts];
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-            uint32_t h, l2;
-            split2(v[2 * q] * scale, v[2 * q + 1] * scale, h, l2);
-            hi[q] = h, lo[q] = l2;
+            uint32_t word[kParts];
+            split_pair(v[2 * q] * scale, v[2 * q + 1] * scale, word);
+#pragma unroll
+            for (int n = 0; n < kParts; ++n) parts[n][q] = word[n];
         }
-        frag[mt][kt][0][l] = hi;
-        frag[mt][kt][1][l] = lo;
+#pragma unroll
+        for (int n = 0; n < kParts; ++n) frag[mt][kt][n][l] = parts[n];
     }
     __syncthreads();
-    const int c0 = tile * 256 + wave * 64;
-    if (c0 >= a.N) return;
-    const int left = a.N - c0 - kg * 16;                 // columns from this lane's first on
-    v4u b[4][KT];
-    int held = -1;
+    // groups of one adapter together, one after another where they differ
 #pragma unroll
-    for (int i = 0; i < RB; ++i) {
-        if (e[i] < 0) continue;
-        if (e[i] != held) {
-            held = e[i];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int n = c0 + (m >> 2) * 16 + q * 4 + (m & 3);
-                const bool in = n < a.N;
-                const uint16_t *row = a.w + ((int64_t)held * a.N + (in ? n : 0)) * a.r;
-#pragma unroll
-                for (int kt = 0; kt < KT; ++kt) {
-                    const int j = kt * 32 + kg * 8;
-                    const v4u v = *reinterpret_cast<const v4u *>(row + (j < a.r ? j : 0));
-                    b[q][kt] = in && j < a.r ? v : v4u{0, 0, 0, 0};
-                }
-            }
-        }
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            const int token = token_of(a.row_token, (int64_t)(rb0 + i) * kRows + t * 16 + m, a.T);
-            if (__ballot(token >= 0) == 0) continue;
-            Y *y = static_cast<Y *>(a.y) + (token < 0 ? 0 : token) * a.ld + c0 + kg * 16;
-            const int take = token < 0 ? 0 : left;
-            Run16<Y> run{};
-            run.load(y, take);
-            v4f d[4] = {v4f{0, 0, 0, 0}, v4f{0, 0, 0, 0}, v4f{0, 0, 0, 0}, v4f{0, 0, 0, 0}};
-#pragma unroll
-            for (int kt = 0; kt < KT; ++kt) {
-                const v4u hi = frag[i * 2 + t][kt][0][lane], lo = frag[i * 2 + t][kt][1][lane];
-#pragma unroll
-                for (int q = 0; q < 4; ++q) d[q] = mfma(b[q][kt], lo, d[q]);
-#pragma unroll
-                for (int q = 0; q < 4; ++q) d[q] = mfma(b[q][kt], hi, d[q]);
-            }
-            run.add_store(y, take, d);
-        }
+    for (int s = 0; s < RB; ++s) {
+        const int adapter = e[s];
+        if (adapter < 0 || (s && adapter == e[s - 1])) continue;
+        if (s != start && first < a.N) ask(ahead[0], adapter, first);
+        if (whole) columns(std::true_type(), ahead, adapter, first, step);
+        else columns(std::false_type(), ahead, adapter, first, step);
     }
 }
 
@@ -430,25 +582,26 @@ struct WideGrid {
     }
 };
 
+constexpr int kOuterParts = 3;
+
 template <int RT, class Wide>
 __device__ __forceinline__ void outer_rows(const LoraOuter &a, const LoraWide &w, const Item &it, float scale, int j0, int col,
                                            bool in, int lane, int wave, v4f (&acc)[RT][8]) {
     const int m = lane & 15, kg = lane >> 4;
-    for (int row = it.row0 + wave * kRows; row < it.row1; row += kWaves * kRows) {
-        const int r0 = row + kg * 8;
-        int token[8];
+    constexpr int kStep = kWaves * kRows;
+    // While a block of 32 rows is used, the next one's values and the tokens of the one after it are on their way.
+    int64_t named[8];
+    auto ask_tokens = [&](int row) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) token[i] = token_of(a.row_token, r0 + i, a.T);
-        Wide x;
+        for (int i = 0; i < 8; ++i) named[i] = a.row_token[row < it.row1 ? row + kg * 8 + i : 0];
+    };
+    auto ask = [&](int row, Wide &x, int (&token)[8]) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) token[i] = named[i] >= 0 && named[i] < a.T && row < it.row1 ? (int)named[i] : -1;
         x.load(w, token, col, in);
-        float p[RT][8];
-#pragma unroll
-        for (int j = 0; j < RT; ++j) {
-            const int rank = j0 + j * 16 + m;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) p[j][i] = w.p[(int64_t)(r0 + i) * a.r + (rank < a.r ? rank : 0)];
-        }
-        v4u hi[RT], lo[RT];
+    };
+    auto use = [&](int row, const Wide &x, const int (&token)[8], const float (&p)[RT][8]) {
+        v4u parts[RT][kOuterParts];
 #pragma unroll
         for (int j = 0; j < RT; ++j)
 #pragma unroll
@@ -456,18 +609,48 @@ __device__ __forceinline__ void outer_rows(const LoraOuter &a, const LoraWide &w
                 // a padding row's p must not meet the zeros that stand for its x as a NaN
                 const float s0 = token[2 * q] >= 0 ? p[j][2 * q] * scale : 0.0f;
                 const float s1 = token[2 * q + 1] >= 0 ? p[j][2 * q + 1] * scale : 0.0f;
-                uint32_t h, l;
-                split2(s0, s1, h, l);
-                hi[j][q] = h, lo[j][q] = l;
+                uint32_t word[kOuterParts];
+                split_pair(s0, s1, word);
+#pragma unroll
+                for (int n = 0; n < kOuterParts; ++n) parts[j][n][q] = word[n];
             }
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
             const v4u f = x.column(c);
 #pragma unroll
-            for (int j = 0; j < RT; ++j) acc[j][c] = mfma(lo[j], f, acc[j][c]);
+            for (int n = kOuterParts - 1; n >= 0; --n)
 #pragma unroll
-            for (int j = 0; j < RT; ++j) acc[j][c] = mfma(hi[j], f, acc[j][c]);
+                for (int j = 0; j < RT; ++j) acc[j][c] = mfma(parts[j][n], f, acc[j][c]);
         }
+    };
+    auto ask_p = [&](int row, float (&p)[RT][8]) {
+#pragma unroll
+        for (int j = 0; j < RT; ++j) {
+            const int rank = j0 + j * 16 + m;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) p[j][i] = w.p[(int64_t)(row + kg * 8 + i) * a.r + (rank < a.r ? rank : 0)];
+        }
+    };
+    Wide x[2];
+    int token[2][8];
+    int row = it.row0 + wave * kRows;
+    // An item without rows may belong to a call without any: nothing at all is read then.  Behind an item's last rows
+    // row 0 of the tables and of x stands in for what would be next.
+    if (row >= it.row1) return;
+    ask_tokens(row);
+    ask(row, x[0], token[0]);
+    ask_tokens(row + kStep);
+    for (; row < it.row1; row += 2 * kStep) {
+        float p[RT][8];
+        ask_p(row, p);
+        ask(row + kStep, x[1], token[1]);
+        ask_tokens(row + 2 * kStep);
+        use(row, x[0], token[0], p);
+        if (row + kStep >= it.row1) break;
+        ask_p(row + kStep, p);
+        ask(row + 2 * kStep, x[0], token[0]);
+        ask_tokens(row + 3 * kStep);
+        use(row + kStep, x[1], token[1], p);
     }
 }
 
@@ -475,20 +658,12 @@ __device__ __forceinline__ void outer_rows(const LoraOuter &a, const LoraWide &w
 // ranks.  A lane loads 8 columns of 8 rows and turns them into eight fragments
 // with one permutation for every two values, so nothing is staged.  Its waves
 // take blocks of 32 rows in turn.
-template <int RT, class WideX>
-__global__ __launch_bounds__(kBlock) void lora_outer_kernel(const LoraOuter a) {
-    __shared__ v4f red[2][RT * 8][64];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+template <int RT, class Wide, bool SECOND>
+__device__ __forceinline__ void outer_block(const LoraOuter &a, const Item &it, int slab, int j0, int lane, int wave,
+                                            v4u (&red)[2][RT * 8][64]) {
+    const LoraWide &w = a.wide[SECOND ? 1 : 0];
     const int m = lane & 15, kg = lane >> 4;
-    const int per = a.wide[0].slabs + a.wide[1].slabs;
-    int at = blockIdx.x % (per * a.passes);
-    const Item it = item_of(a, blockIdx.x / (per * a.passes), lane);
-    if (it.e < 0 || it.slot >= a.slots) return;          // the whole block
-    const int j0 = at / per * RT * 16;
-    at %= per;
-    const bool second = at >= a.wide[0].slabs;
-    const LoraWide &w = a.wide[second ? 1 : 0];
-    const int col = (second ? at - a.wide[0].slabs : at) * 128 + m * 8;
+    const int col = slab * 128 + m * 8;
     const bool in = col < w.C;
     const float scale = a.scales ? a.scales[it.e] : 1.0f;
     v4f acc[RT][8];
@@ -496,23 +671,22 @@ __global__ __launch_bounds__(kBlock) void lora_outer_kernel(const LoraOuter a) {
     for (int j = 0; j < RT; ++j)
 #pragma unroll
         for (int c = 0; c < 8; ++c) acc[j][c] = v4f{0, 0, 0, 0};
-    if (second) outer_rows<RT, WideBf16>(a, w, it, scale, j0, col, in, lane, wave, acc);
-    else outer_rows<RT, WideX>(a, w, it, scale, j0, col, in, lane, wave, acc);
+    outer_rows<RT, Wide>(a, w, it, scale, j0, col, in, lane, wave, acc);
 
     // the four waves' sums, always in the same order: (0 + 2) + (1 + 3)
     if (wave >= 2) {
 #pragma unroll
-        for (int i = 0; i < RT * 8; ++i) red[wave - 2][i][lane] = acc[i >> 3][i & 7];
+        for (int i = 0; i < RT * 8; ++i) red[wave - 2][i][lane] = __builtin_bit_cast(v4u, acc[i >> 3][i & 7]);
     }
     __syncthreads();
     if (wave < 2) {
 #pragma unroll
-        for (int i = 0; i < RT * 8; ++i) acc[i >> 3][i & 7] += red[wave][i][lane];
+        for (int i = 0; i < RT * 8; ++i) acc[i >> 3][i & 7] += __builtin_bit_cast(v4f, red[wave][i][lane]);
     }
     __syncthreads();
     if (wave == 1) {
 #pragma unroll
-        for (int i = 0; i < RT * 8; ++i) red[0][i][lane] = acc[i >> 3][i & 7];
+        for (int i = 0; i < RT * 8; ++i) red[0][i][lane] = __builtin_bit_cast(v4u, acc[i >> 3][i & 7]);
     }
     __syncthreads();
     if (wave != 0 || !in) return;
@@ -524,8 +698,8 @@ __global__ __launch_bounds__(kBlock) void lora_outer_kernel(const LoraOuter a) {
         if (rank >= a.r) continue;
         v4f v[8];
 #pragma unroll
-        for (int c = 0; c < 8; ++c) v[c] = acc[j][c] + red[0][j * 8 + c][lane];
-        if (second) {                                    // [C][r]
+        for (int c = 0; c < 8; ++c) v[c] = acc[j][c] + __builtin_bit_cast(v4f, red[0][j * 8 + c][lane]);
+        if constexpr (SECOND) {                          // [C][r]
 #pragma unroll
             for (int c = 0; c < 8; ++c) *reinterpret_cast<v4f *>(out + (int64_t)(col + c) * a.r + rank) = v[c];
         } else {                                         // [r][C]
@@ -537,6 +711,20 @@ __global__ __launch_bounds__(kBlock) void lora_outer_kernel(const LoraOuter a) {
             }
         }
     }
+}
+
+template <int RT, class WideX>
+__global__ __launch_bounds__(kBlock) void lora_outer_kernel(const LoraOuter a) {
+    __shared__ v4u red[2][RT * 8][64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int per = a.wide[0].slabs + a.wide[1].slabs;
+    int at = blockIdx.x % (per * a.passes);
+    const Item it = item_of(a, blockIdx.x / (per * a.passes), lane);
+    if (it.e < 0 || it.slot >= a.slots) return;          // the whole block
+    const int j0 = at / per * RT * 16;
+    at %= per;
+    if (at >= a.wide[0].slabs) outer_block<RT, WideBf16, true>(a, it, at - a.wide[0].slabs, j0, lane, wave, red);
+    else outer_block<RT, WideX, false>(a, it, at, j0, lane, wave, red);
 }
 
 // The sums of adapters with several items, slots in order; block row y is the
@@ -563,22 +751,40 @@ __global__ __launch_bounds__(kBlock) void lora_join_kernel(const LoraOuter a) {
     const LoraWide &w = a.wide[second ? 1 : 0];
     const int64_t size = second ? size1 : size0, at = second ? i - size0 : i;
     const float *p = w.part + slot * size + at;
-    v4f v = *reinterpret_cast<const v4f *>(p);
-    for (int n = 1; n < m && slot + n < a.slots; ++n) v += *reinterpret_cast<const v4f *>(p + n * size);
+    m = min(m, a.slots - slot);
+    v4f v = {0, 0, 0, 0};
+    for (int n0 = 0; n0 < m; n0 += 8) {                  // eight in flight
+        v4f part[8];
+#pragma unroll
+        for (int n = 0; n < 8; ++n) part[n] = *reinterpret_cast<const v4f *>(p + (n0 + n < m ? n0 + n : 0) * size);
+#pragma unroll
+        for (int n = 0; n < 8; ++n)
+            if (n0 + n < m) v += part[n];
+    }
     *reinterpret_cast<v4f *>(w.out + e * size + at) = v;
 }
 
 template <class Y, int KT>
-void start_expand(LoraExpand a, bool wide, hipStream_t stream) {
-    const int64_t blocks = a.rows / kRows;
-    if (wide) lora_expand_kernel<Y, KT, 4><<<(unsigned)(ceil_div(blocks, 4) * a.tiles), kBlock, 0, stream>>>(a);
-    else lora_expand_kernel<Y, KT, 1><<<(unsigned)(blocks * a.tiles), kBlock, 0, stream>>>(a);
+void start_expand(LoraExpand a, int cus, hipStream_t stream) {
+    // Blocks of 64 rows (32 where y is fp32) that go through several columns each, as many as are resident at once (by
+    // their registers two a compute unit, one for ranks above 64), where there are that many columns; else of 32 rows
+    // and 256 columns.
+    constexpr int kWide = sizeof(Y) == 4 ? 1 : 2, kResident = KT == 4 ? 1 : 2;
+    const int64_t blocks = a.rows / kRows, groups = ceil_div(blocks, kWide), tiles = a.N ? ceil_div(a.N, 256) : 1;
+    if (groups * tiles >= 2 * kResident * cus) {
+        const int64_t step = kResident * cus / groups;
+        a.step = (int)(step > 1 ? step : 1);
+        lora_expand_kernel<Y, KT, kWide, true><<<(unsigned)(groups * a.step), kBlock, 0, stream>>>(a);
+    } else {
+        a.step = (int)tiles;
+        lora_expand_kernel<Y, KT, 1, false><<<(unsigned)(blocks * tiles), kBlock, 0, stream>>>(a);
+    }
 }
 template <class Y>
-void start_expand(const LoraExpand &a, bool wide, hipStream_t stream) {
-    if (a.r <= 32) start_expand<Y, 1>(a, wide, stream);
-    else if (a.r <= 64) start_expand<Y, 2>(a, wide, stream);
-    else start_expand<Y, 4>(a, wide, stream);
+void start_expand(const LoraExpand &a, int cus, hipStream_t stream) {
+    if (a.r <= 32) start_expand<Y, 1>(a, cus, stream);
+    else if (a.r <= 64) start_expand<Y, 2>(a, cus, stream);
+    else start_expand<Y, 4>(a, cus, stream);
 }
 template <int RT>
 void start_outer(const LoraOuter &a, int form, unsigned grid, hipStream_t stream) {
@@ -591,7 +797,7 @@ void start_outer(const LoraOuter &a, int form, unsigned grid, hipStream_t stream
 
 LoraCut lora_cut(int64_t rows, int64_t K, int cus) {
     // blocks of 32 rows; the wide axis is cut where they alone do not fill the compute units twice, into slices that
-    // give every wave of a block a chunk of 128
+    // give every wave of a block a chunk
     const int64_t blocks = rows / kRows, most = ceil_div(K, kWaves * 128);
     int64_t splits = blocks ? ceil_div(2 * cus, blocks) : 1;
     splits = splits < most ? splits : most;
@@ -610,10 +816,9 @@ hipError_t launch_lora_shrink(const LoraShrink &a, hipStream_t stream) {
 }
 
 hipError_t launch_lora_expand(LoraExpand a, bool y_bf16, hipStream_t stream) {
-    a.tiles = (int)(a.N ? ceil_div(a.N, 256) : 1);       // N = 0: P alone
-    const bool wide = a.rows / kRows * a.tiles >= 16 * (int64_t)device_cu_count();
-    if (y_bf16) start_expand<uint16_t>(a, wide, stream);
-    else start_expand<float>(a, wide, stream);
+    const int cus = device_cu_count();
+    if (y_bf16) start_expand<uint16_t>(a, cus, stream);
+    else start_expand<float>(a, cus, stream);
     return hipGetLastError();
 }
 
@@ -630,7 +835,7 @@ hipError_t launch_lora_transpose(const LoraTranspose &a, hipStream_t stream) {
 
 LoraOuterPlan lora_outer_plan(int64_t rows, int64_t E, int64_t r, int64_t K, int64_t N, int cus) {
     const int64_t passes = ceil_div(r, 64), slabs = (ceil_div(K, 128) + ceil_div(N, 128)) * passes;
-    const int64_t wanted = slabs < 4 * cus ? 4 * cus / slabs : 1;
+    const int64_t wanted = slabs < 2 * cus ? 2 * cus / slabs : 1;
     int64_t chunk = ceil_div(ceil_div(rows, wanted), kWaves * kRows) * kWaves * kRows;
     chunk = chunk > 256 ? chunk : 256;
     const int64_t items = rows / chunk + E;

@@ -288,8 +288,8 @@ struct LoraExpand {
     int64_t rows;
     const float *part;          // [splits][rows][r]
     float *hidden;              // [rows][r] or null: the sum of the partials
-    int E, r, N, splits;
-    int tiles;                  // set by the launcher
+    int E, r, N, splits;        // N = 0: hidden alone
+    int step;                   // set by the launcher: blocks beside each other on the same rows
 };
 hipError_t launch_lora_expand(LoraExpand a, bool y_bf16, hipStream_t stream);
 struct LoraTranspose {

@@ -9,7 +9,7 @@ CUS = 256
 def plan(rows, E, r, K, N):
     passes = -(-r // 64)
     slabs = (-(-K // 128) + -(-N // 128)) * passes
-    wanted = max(1, 4 * CUS // slabs)
+    wanted = max(1, 2 * CUS // slabs)
     chunk = max(256, -(-(-(-rows // wanted)) // 128) * 128)
     items = rows // chunk + E
     return chunk, items, min(2 * rows // chunk, items)
