@@ -1,8 +1,9 @@
 /*
  * mxfp8_policy.h -- C ABI of the operators that a policy trained and sampled
  * with low-rank adapters needs around the MXFP8 layers: the gated activation
- * with its inputs kept in 8 bits for the backward pass, and the adapters
- * beside a shared projection with their gradients.
+ * with its inputs kept in 8 bits for the backward pass, the adapters beside a
+ * shared projection with their gradients, and the verification of drafted
+ * tokens.
  *
  * The conventions of mxfp8.h hold (row-major, caller-owned buffers, host
  * validation before anything is enqueued, one stream, no allocation, no
@@ -136,6 +137,58 @@ mxfp8_status mxfp8_lora_backward(void *d_x_bf16, int64_t ld_dx, const void *d_y_
                                  const int32_t *offsets, const int64_t *row_token, int64_t rows, const float *hidden,
                                  float *d_a, float *d_b, void *workspace, size_t workspace_bytes,
                                  hipStream_t stream);
+
+/* Workspace bytes of mxfp8_verify_drafts, with or without draft logits (0 for
+ * invalid sizes). */
+size_t mxfp8_verify_drafts_workspace_bytes(int64_t R, int64_t B, int64_t V, int draft_logits);
+
+/*
+ * mxfp8_verify_drafts -- which drafted tokens of each request stand, and the
+ * token that follows them, from given random numbers; the tokens that come out
+ * are distributed as if the target had been sampled.
+ *
+ * Request b has the rows [offsets[b], offsets[b+1]) of the target's logits: one
+ * for each of its n drafted tokens, in order, and one after the last.  With
+ * p = softmax(logits / temperature) of a row, q = softmax(draft_logits /
+ * temperature) of the drafted token's row (1 at the token itself where
+ * draft_logits is NULL: a draft that was looked up, not drawn), x the drafted
+ * token and u its uniform:
+ *   the drafted tokens stand up to the first with  not (u q(x) < p(x));
+ *   the next token is the column with the largest w / noise, lowest first, of
+ *     w = max(p - q, 0) at that position, or of w = p after the last draft;
+ *     columns with w / noise not above 0 are not drawn
+ * noise holds exponential draws (rate 1), so the column is drawn with
+ * probability w / sum w.  Where p exceeds q nowhere (rounding, or a draft row
+ * without a distribution), w = p.  The decisions are those of probabilities
+ * held in fp64 (close ones are taken again in fp64), with noise of 2^-32 to
+ * 2^32.  A temperature near 0 (2^-60) with draft_logits NULL compares with the
+ * largest logit: greedy verification.
+ *
+ *   accepted [B] int32 : drafted tokens that stand
+ *   tokens   [R] int64 : by row: the drafted tokens that stand, the next one,
+ *     then -1
+ *   logprobs [R] FP32  : log p of those tokens, 0 behind them
+ * A row without a distribution (a NaN or +Inf in it, or nothing above -Inf)
+ * lets no draft stand and gives no token: -1, log-probability NaN.  A drafted
+ * token outside [0, V) does not stand.
+ *
+ *   logits : FP32 or BF16 [R][V], rows ld apart; draft_logits : the same dtype
+ *     [R - B][V], rows ld_draft apart, or NULL; row offsets[b] - b + i is that
+ *     of request b's i-th drafted token, as for
+ *   draft_ids int64 [R - B], uniforms FP32 [R - B] in [0, 1)
+ *   noise : FP32 [B][V], rows ld_noise apart
+ *   offsets : DEVICE int32 [B+1], rising by at least 1, offsets[0] == 0,
+ *     offsets[B] == R.  Entries are clamped to [0, R]; a request without rows
+ *     has accepted 0 and no token; rows of no request are not written
+ *   workspace : mxfp8_verify_drafts_workspace_bytes(..) bytes, 16-byte aligned
+ * B >= 0 (0 enqueues nothing), B <= R < 2^31, 1 <= V < 2^31, 2^-60 <= temperature
+ * <= 2^60, (2 R - B) * ceil(V / 4096) < 2^22; pointers aligned as their elements.
+ */
+mxfp8_status mxfp8_verify_drafts(const void *logits, mxfp8_dtype dtype, int64_t ld, int64_t R, int64_t V,
+                                 const int32_t *offsets, int64_t B, const int64_t *draft_ids, const float *uniforms,
+                                 const void *draft_logits, int64_t ld_draft, const float *noise, int64_t ld_noise,
+                                 double temperature, int32_t *accepted, int64_t *tokens, float *logprobs,
+                                 void *workspace, size_t workspace_bytes, hipStream_t stream);
 
 #ifdef __cplusplus
 }

@@ -948,6 +948,8 @@ __all__ += ["route", "route_backward", "route_rows", "route_tables", "RouteTable
 # ------------------------------------------------------------------ checkpoints, adapters, drafts
 
 from .checkpoint import Swiglu, swiglu, swiglu_backward  # noqa: E402
+from .drafts import DraftVerdict, verify_drafts  # noqa: E402
 from .lora import lora_add_, lora_backward_  # noqa: E402
 
-__all__ += ["swiglu", "swiglu_backward", "Swiglu", "lora_add_", "lora_backward_"]
+__all__ += ["swiglu", "swiglu_backward", "Swiglu", "lora_add_", "lora_backward_",
+            "verify_drafts", "DraftVerdict"]

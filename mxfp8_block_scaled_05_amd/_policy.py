@@ -26,7 +26,10 @@ def policy_lib():
             ("mxfp8_lora_add", [P, I32, I64, P, I64, I64, P, P, P, I64, I64, I64, I64, P, P, I64, P, P, SZ, P], I32),
             ("mxfp8_lora_backward_workspace_bytes", [I64] * 5, SZ),
             ("mxfp8_lora_backward", [P, I64, P, I64, P, P, I32, I64, I64, P, P, P, I64, I64, I64, I64, P, P, I64, P, P,
-                                     P, P, SZ, P], I32)):
+                                     P, P, SZ, P], I32),
+            ("mxfp8_verify_drafts_workspace_bytes", [I64, I64, I64, I32], SZ),
+            ("mxfp8_verify_drafts", [P, I32, I64, I64, I64, P, I64, P, P, P, I64, P, I64, ctypes.c_double, P, P, P, P, SZ,
+                                     P], I32)):
         f = getattr(L, name)
         f.argtypes, f.restype = args, res
     _ready = L

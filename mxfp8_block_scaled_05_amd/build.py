@@ -22,7 +22,7 @@ LIB = os.path.join(PKG, "libmxfp8.so")
 
 SOURCES = ["api.cpp", "quantize.hip", "dequantize.hip", "repack.hip", "gemm.hip", "selfcheck.hip",
            "api_tokens.cpp", "route.hip", "tables.hip", "combine.hip", "logprobs.hip",
-           "api_policy.cpp", "swiglu.hip", "lora.hip"]
+           "api_policy.cpp", "swiglu.hip", "lora.hip", "drafts.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",
          "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",

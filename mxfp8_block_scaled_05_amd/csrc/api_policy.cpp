@@ -35,6 +35,10 @@ bool lora_sizes_ok(int64_t rows, int64_t E, int64_t r, int64_t K, int64_t N) {
            (rows / 256 + E) * ceil_div(K + N, 128) < ((int64_t)1 << 22) && E * r * (K + N) < ((int64_t)1 << 40);
 }
 
+bool drafts_sizes_ok(int64_t R, int64_t B, int64_t V) {
+    return B >= 0 && R >= B && R < kMaxInt && V >= 1 && V < kMaxInt && (2 * R - B) * ceil_div(V, 4096) < ((int64_t)1 << 22);
+}
+
 // The parts of a workspace, in order, each from a multiple of 256 bytes on.
 struct Parts {
     int64_t at = 0;
@@ -210,6 +214,43 @@ mxfp8_status mxfp8_lora_backward(void *d_x, int64_t ld_dx, const void *d_y, int6
     o.wide[1] = {hidden, d_y, nullptr, ld_dy, 0, (int)N, d_b, reinterpret_cast<float *>(base + w.slots_b), 0};
     o.scales = scales, o.offsets = offsets, o.row_token = row_token, o.rows = used, o.T = T, o.E = (int)E, o.r = (int)r;
     return finish(launch_lora_outer(o, w.plan, form, stream));
+}
+
+size_t mxfp8_verify_drafts_workspace_bytes(int64_t R, int64_t B, int64_t V, int draft_logits) {
+    if (!drafts_sizes_ok(R, B, V) || B == 0) return 0;
+    return (size_t)draft_cut(draft_logits ? 2 * R - B : R, B, V, device_cu_count()).bytes;
+}
+
+mxfp8_status mxfp8_verify_drafts(const void *logits, mxfp8_dtype dtype, int64_t ld, int64_t R, int64_t V,
+                                 const int32_t *offsets, int64_t B, const int64_t *draft_ids, const float *uniforms,
+                                 const void *draft_logits, int64_t ld_draft, const float *noise, int64_t ld_noise,
+                                 double temperature, int32_t *accepted, int64_t *tokens, float *logprobs,
+                                 void *workspace, size_t workspace_bytes, hipStream_t stream) {
+    if (raw(dtype) != MXFP8_F32 && raw(dtype) != MXFP8_BF16) return MXFP8_ERR_DTYPE;
+    if (!drafts_sizes_ok(R, B, V) || !rows_ok(R, V, ld) || !rows_ok(B, V, ld_noise)) return MXFP8_ERR_SHAPE;
+    const int64_t D = R - B, e = raw(dtype) == MXFP8_BF16 ? 2 : 4;
+    if (draft_logits && !rows_ok(D, V, ld_draft)) return MXFP8_ERR_SHAPE;
+    if (!(temperature >= 0x1p-60 && temperature <= 0x1p60)) return MXFP8_ERR_SHAPE;
+    if (B == 0) return MXFP8_OK;
+    if (!logits || !offsets || !noise || !accepted || !tokens || !logprobs || !workspace || (D && (!draft_ids || !uniforms)))
+        return MXFP8_ERR_NULL;
+    const void *draft = D ? draft_logits : nullptr;
+    const int64_t rows = draft ? R + D : R, need = draft_cut(rows, B, V, device_cu_count()).bytes;
+    if ((int64_t)workspace_bytes < need) return MXFP8_ERR_SHAPE;
+    if (!aligned(logits, e) || !aligned(draft_logits, e) || !aligned(offsets, 4) || !aligned(draft_ids, 8) || !aligned(uniforms, 4) ||
+        !aligned(noise, 4) || !aligned(accepted, 4) || !aligned(tokens, 8) || !aligned(logprobs, 4) || !aligned(workspace, 16))
+        return MXFP8_ERR_ALIGN;
+    if (overlap({{accepted, B * 4}, {tokens, R * 8}, {logprobs, R * 4}, {workspace, need}},
+                {{logits, R, V * e, ld * e}, {draft, D, V * e, ld_draft * e}, {offsets, (B + 1) * 4}, {draft_ids, D * 8},
+                 {uniforms, D * 4}, {noise, B, V * 4, ld_noise * 4}}))
+        return MXFP8_ERR_OVERLAP;
+    mxfp8_status st = check_device();
+    if (st != MXFP8_OK) return st;
+    DraftArgs a{};
+    a.x = logits, a.ld = ld, a.R = R, a.V = V, a.B = B, a.offsets = offsets, a.ids = draft_ids, a.u = uniforms;
+    a.d = draft, a.ld_d = ld_draft, a.noise = noise, a.ld_n = ld_noise, a.temperature = temperature;
+    a.accepted = accepted, a.tokens = tokens, a.logprobs = logprobs, a.workspace = workspace, a.rows = rows;
+    return finish(launch_drafts(a, e == 2, stream));
 }
 
 }  // extern "C"

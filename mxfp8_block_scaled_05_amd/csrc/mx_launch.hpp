@@ -328,6 +328,37 @@ struct LoraOuter {
 // form of the first wide matrix: 0 bf16, 1 canonical grid, 2 packed
 hipError_t launch_lora_outer(LoraOuter a, const LoraOuterPlan &plan, int form, hipStream_t stream);
 
+// Verification of drafted tokens (drafts.hip).  B >= 1.
+struct DraftArgs {
+    const void *x;              // the target's logits [R][ld]
+    int64_t ld, R, V, B;
+    const int32_t *offsets;     // [B + 1]
+    const int64_t *ids;         // [R - B]
+    const float *u;             // [R - B]
+    const void *d;              // the draft's logits [R - B][ld_d] or null
+    int64_t ld_d;
+    const float *noise;         // [B][ld_n]
+    int64_t ld_n;
+    double temperature;
+    int32_t *accepted;          // [B]
+    int64_t *tokens;            // [R]
+    float *logprobs;            // [R]
+    void *workspace;
+    int64_t rows;               // R, and with the draft's logits R - B more
+    // set by the launcher
+    double inv_temperature, scale64;        // 1 / temperature, log2(e) / temperature
+    float scale;
+    int64_t slice, cut;
+    int slices, cuts;
+};
+// slices of a row's sums, cuts of a request's race, their lengths, and the workspace they take
+struct DraftCut {
+    int slices, cuts;
+    int64_t slice, cut, bytes;
+};
+DraftCut draft_cut(int64_t rows, int64_t B, int64_t V, int cus);
+hipError_t launch_drafts(DraftArgs a, bool bf16, hipStream_t stream);
+
 // Packed weight layout geometry (see mxfp8_repack in include/mxfp8.h).
 constexpr int64_t kPanelRows = 256;   // rows per packed panel
 constexpr int64_t kKStep = 128;       // K bytes per packed k-step (one MFMA K)
