@@ -3,14 +3,16 @@
 //
 //   rows    max and sum of e^((x - max) / temp) of every row of the target's
 //           and the draft's logits: one pass over all of them
-//   draw    of the row at which each request stops: the race of w / noise,
+//   draw    where each request stops, and the race of w / noise at that row,
 //           split over blocks
-//   finish  joins the race, writes the tokens and their log-probabilities
+//   finish  joins the race and writes the token (by the last block of a race
+//           instead: 64 requests 106 us for 50, since the fences that it needs
+//           write back and empty each XCD's L2)
 //
 // Whether a token stands, and which column wins, are decisions of whole
 // numbers that a last bit can turn.  They are taken from fp32 exponentials
 // with a bound of what those may be off by; where the bound leaves two
-// outcomes (about 1 request in 10^4), finish takes the decision again in fp64.
+// outcomes (about 1 request in 10^4), the decision is taken again in fp64.
 //
 // Bounds.  A term's exponent carries three roundings of |u| 2^-24 (distance,
 // scale, product), u its distance from the maximum in powers of two.  Averaged
@@ -18,6 +20,8 @@
 // are added in fp64, is within 31 * 3 * ln 2 * 2^-24 + 2^-21 < 2^-17 of its
 // value (2^-18 at 2^17 columns).  A single term of |u| <= 126 is within
 // 126 * 3 * ln 2 * 2^-24 + 2^-22 < 2^-15.9; below it is 0.
+#include <type_traits>
+
 #include "mx_launch.hpp"
 #include "mx_wave.hpp"
 
@@ -27,6 +31,7 @@ namespace {
 
 constexpr int kBlock = 256;
 constexpr int kUnroll = 4;
+constexpr int kDrawBlocks = 4;              // of the race resident on a compute unit
 constexpr float kLowest = -3.402823466e38f;
 constexpr float kDrawSlack = 0x1p-15f;      // of p and q as the race sees them
 constexpr double kStandSlack = 0x1p-16;     // of p(x) and u q(x): their terms in fp64, the rows' sums as above
@@ -35,6 +40,9 @@ constexpr double kStandSlack = 0x1p-16;     // of p(x) and u q(x): their terms i
 struct RowSum {
     float m;
     double s;
+};
+struct Pair {
+    RowSum p, q;
 };
 struct Part {                               // of a slice of a row, in the workspace
     float m, pad;
@@ -46,15 +54,23 @@ __device__ __forceinline__ Part *parts_of(const DraftArgs &a) { return static_ca
 // (-1: no w above 0), and the next largest.
 struct Race {
     float best, second;
-    int64_t column;
+    int column;
 };
-__device__ __forceinline__ Race *races_of(const DraftArgs &a) {
-    return reinterpret_cast<Race *>(parts_of(a) + a.rows * a.slices);
+// What the fast sums say about a request, from its first draw block to finish.
+struct Verdict {
+    int end;                                // drafted tokens that stand
+    int open;                               // finish takes the decisions and writes the tokens
+    Pair rows;                              // at which it stops
+};
+__device__ __forceinline__ Verdict *verdicts_of(const DraftArgs &a) {
+    return reinterpret_cast<Verdict *>(parts_of(a) + a.rows * a.slices);
 }
+__device__ __forceinline__ Race *races_of(const DraftArgs &a) { return reinterpret_cast<Race *>(verdicts_of(a) + a.B); }
 
+template <int W>
 __device__ __forceinline__ double sum_lanes(double v) {
 #pragma unroll
-    for (int d = 32; d; d >>= 1) v += __shfl_xor(v, d, 64);
+    for (int d = W / 2; d; d >>= 1) v += __shfl_xor(v, d, 64);
     return v;
 }
 
@@ -124,7 +140,7 @@ __global__ __launch_bounds__(BLOCK) void draft_rows_kernel(const DraftArgs a) {
         take<kV>(v, x, c);
     }
     const float m = group_reduce<64>(v.m, OpMax());
-    const double s = sum_lanes(v.s * (double)__builtin_amdgcn_exp2f((v.m - m) * c));
+    const double s = sum_lanes<64>(v.s * (double)__builtin_amdgcn_exp2f((v.m - m) * c));
     if (lane == 0) parts[wave] = Part{m, 0.0f, s};
     __syncthreads();
     if (threadIdx.x != 0) return;
@@ -135,18 +151,25 @@ __global__ __launch_bounds__(BLOCK) void draft_rows_kernel(const DraftArgs a) {
     parts_of(a)[blockIdx.x] = p;
 }
 
-// The joined slices of row i; all lanes of a wave, all get it.  A row with a
-// NaN or +Inf, or nothing above -Inf, has s = NaN.
-__device__ __forceinline__ RowSum join_row(const DraftArgs &a, int64_t i, int lane) {
-    const Part *p = parts_of(a) + i * a.slices;
-    float m = kLowest;
-    for (int k = lane; k < a.slices; k += 64) m = __builtin_fmaxf(m, p[k].m);
-    m = group_reduce<64>(m, OpMax());
-    double s = 0.0;
-    for (int k = lane; k < a.slices; k += 64) s += p[k].s * exp2(((double)p[k].m - m) * a.scale64);
-    s = sum_lanes(s);
+// The joined slices of two rows (the second may be none, -1: sum 1), half a
+// wave each; all lanes get both.  A row with a NaN or +Inf, or nothing above
+// -Inf, has s = NaN.
+__device__ __forceinline__ Pair join_rows(const DraftArgs &a, int64_t i, int64_t j, int lane) {
+    const int64_t row = lane < 32 || j < 0 ? i : j;
+    const Part *part = parts_of(a) + row * a.slices;
+    const int l = lane & 31;
+    Part held = part[l < a.slices ? l : 0];              // at most 32 of them as a rule
+    if (l >= a.slices) held.s = 0.0;
+    float m = held.m;
+    for (int k = l + 32; k < a.slices; k += 32) m = __builtin_fmaxf(m, part[k].m);
+    m = group_reduce<32>(m, OpMax());
+    double s = held.s * exp2(((double)held.m - m) * a.scale64);
+    for (int k = l + 32; k < a.slices; k += 32) s += part[k].s * exp2(((double)part[k].m - m) * a.scale64);
+    s = sum_lanes<32>(s);
     if (!(s > 0.0) || m > -kLowest) s = __builtin_nan("");
-    return {m, s};
+    Pair r{{__shfl(m, 0, 64), __shfl(s, 0, 64)}, {__shfl(m, 32, 64), __shfl(s, 32, 64)}};
+    if (j < 0) r.q = RowSum{0.0f, 1.0};
+    return r;
 }
 
 // p or q of a logit of a row, in fp64 but for the row's sum
@@ -171,44 +194,58 @@ __device__ __forceinline__ Request request_of(const DraftArgs &a, int64_t b) {
 }
 
 // Whether drafted token i of a request stands; close: fp64 sums might say
-// otherwise.  All lanes of a wave.
+// otherwise.
 struct Stand {
     bool stands, close;
+    int64_t id;
+    float logprob;
 };
+__device__ __forceinline__ float log_share(const DraftArgs &a, double x, const RowSum &r) {
+    return (float)((x - r.m) * a.inv_temperature - log(r.s));
+}
 template <class E>
-__device__ __forceinline__ Stand stand_of(const DraftArgs &a, const Request &r, int i, const RowSum &p_row, const RowSum &q_row) {
+__device__ __forceinline__ Stand stand_of(const DraftArgs &a, const Request &r, int i, int64_t x, double u, const Pair &rows) {
+    if (x < 0 || x >= a.V) return {false, false, x, 0.0f};
+    const double z = Elem<E>::get(row_of<E>(a, r.first + i)[x]);
+    const double p = share(a, z, rows.p);
+    const double q = a.d ? share(a, Elem<E>::get(row_of<E>(a, a.R + r.draft + i)[x]), rows.q) : 1.0;
+    const double uq = u * q;
+    return {uq < p, uq + p > 0.0 && __builtin_fabs(uq - p) <= kStandSlack * (uq + p), x, log_share(a, z, rows.p)};
+}
+// that of the rows' fast sums; all lanes of a wave
+template <class E>
+__device__ __forceinline__ Stand fast_stand(const DraftArgs &a, const Request &r, int i, int lane, Pair &rows) {
     const int64_t x = a.ids[r.draft + i];
-    if (x < 0 || x >= a.V) return {false, false};
-    const double p = share(a, Elem<E>::get(row_of<E>(a, r.first + i)[x]), p_row);
-    const double q = a.d ? share(a, Elem<E>::get(row_of<E>(a, a.R + r.draft + i)[x]), q_row) : 1.0;
-    const double uq = (double)a.u[r.draft + i] * q;
-    return {uq < p, uq + p > 0.0 && __builtin_fabs(uq - p) <= kStandSlack * (uq + p)};
+    const float u = a.u[r.draft + i];
+    rows = join_rows(a, r.first + i, a.d ? a.R + r.draft + i : -1, lane);
+    return stand_of<E>(a, r, i, x, u, rows);
 }
 
-// Where each request stops by the fast sums.  The whole block; `found` is LDS.
-// end: the first drafted token that does not stand, or their number; close:
-// a decision up to there needs fp64.
-struct Stop {
-    int end;
-    bool close;
+// Where a request of at most kHeld drafted tokens stops by the fast sums, with
+// the sums of all its rows.  In LDS, by the whole block.
+constexpr int kHeld = 31;
+struct Held {
+    int refused, close;             // the first of each
+    Pair rows[kHeld + 1];
+    Stand stand[kHeld + 1];
 };
-template <class E, int BLOCK>
-__device__ __forceinline__ Stop stop_of(const DraftArgs &a, const Request &r, int (&found)[2]) {
+template <class E>
+__device__ __forceinline__ void hold(const DraftArgs &a, const Request &r, Held &h) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    if (threadIdx.x < 2) found[threadIdx.x] = r.drafts < 0 ? 0 : r.drafts;
+    if (threadIdx.x == 0) h.refused = h.close = r.drafts;
     __syncthreads();
-    for (int i = wave; i < r.drafts; i += BLOCK / 64) {
-        const RowSum p = join_row(a, r.first + i, lane);
-        RowSum q{0.0f, 1.0};
-        if (a.d) q = join_row(a, a.R + r.draft + i, lane);
-        const Stand s = stand_of<E>(a, r, i, p, q);
-        if (lane == 0 && !s.stands) atomicMin(&found[0], i);
-        if (lane == 0 && s.close) atomicMin(&found[1], i);
+    for (int i = wave; i <= r.drafts; i += kBlock / 64) {
+        Pair rows;
+        Stand s{true, false, -1, 0.0f};
+        if (i < r.drafts) s = fast_stand<E>(a, r, i, lane, rows);
+        else rows = join_rows(a, r.first + i, -1, lane);
+        if (lane == 0) {
+            h.rows[i] = rows, h.stand[i] = s;
+            if (!s.stands) atomicMin(&h.refused, i);
+            if (s.close) atomicMin(&h.close, i);
+        }
     }
     __syncthreads();
-    const Stop stop{found[0], found[1] <= found[0] && found[1] < r.drafts};
-    __syncthreads();
-    return stop;
 }
 
 __device__ __forceinline__ void merge(Race &v, const Race &o) {
@@ -224,85 +261,156 @@ __device__ __forceinline__ Race merge_lanes(Race v) {
     return v;
 }
 
+// ---------------------------------------------------------------- draw
+
 // A cut of the race at the row where a request stops.  Every column's upper
 // bound of w / noise, with w = p - q; the column that wins does so for certain
-// if its lower bound is above the next upper bound.
+// if its lower bound is above the next upper bound.  A request's first block
+// writes the drafted tokens that stand and what is behind the next one.
 template <class E>
-__global__ __launch_bounds__(kBlock) void draft_draw_kernel(const DraftArgs a) {
-    constexpr int kV = Elem<E>::kVec, kWaves = kBlock / 64;
-    __shared__ int found[2];
-    __shared__ Race races[kWaves];
+__global__ __launch_bounds__(kBlock, kDrawBlocks) void draft_draw_kernel(const DraftArgs a) {
+    constexpr int kV = Elem<E>::kVec, kStep = kBlock * kV;
+    __shared__ Held held;
+    __shared__ Race races[kBlock / 64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int64_t b = blockIdx.x / a.cuts;
     const int cut = (int)(blockIdx.x - b * a.cuts);
     const Request r = request_of(a, b);
     if (r.drafts < 0) return;
-    const Stop stop = stop_of<E, kBlock>(a, r, found);
-    if (stop.close) return;                              // finish does it all
-    const int64_t at = r.first + stop.end, drafted = r.draft + stop.end;
-    const bool refused = stop.end < r.drafts, with_q = refused && a.d;
-    const RowSum pr = join_row(a, at, lane);
-    RowSum qr{0.0f, 1.0};
-    if (with_q) qr = join_row(a, a.R + drafted, lane);
-    const int64_t taken = refused && !a.d ? a.ids[drafted] : -1;
-    const float pk = (float)((1.0 + kDrawSlack) / pr.s), qk = with_q ? (float)((1.0 - kDrawSlack) / qr.s) : 0.0f;
+    Verdict &verdict = verdicts_of(a)[b];
+    bool open = r.drafts > kHeld;
+    if (!open) {
+        hold<E>(a, r, held);
+        open = held.close <= held.refused && held.close < r.drafts;
+    }
+    if (cut == 0 && threadIdx.x == 0) {
+        verdict.end = open ? 0 : held.refused, verdict.open = open;
+        if (!open) verdict.rows = held.rows[held.refused];
+    }
+    if (open) return;
+    const int end = held.refused;
+    if (cut == 0 && threadIdx.x <= r.drafts && threadIdx.x != end) {
+        const Stand s = held.stand[threadIdx.x];
+        const bool stands = (int)threadIdx.x < end;
+        a.tokens[r.first + threadIdx.x] = stands ? s.id : -1;
+        a.logprobs[r.first + threadIdx.x] = stands ? s.logprob : 0.0f;
+    }
+    const int64_t at = r.first + end, drafted = r.draft + end;
+    const bool refused = end < r.drafts, with_q = refused && a.d;
+    const Pair rows = held.rows[end];
+    const int64_t named = held.stand[end].id;
+    const int taken = refused && !a.d && named >= 0 && named < a.V ? (int)named : -1;
+    const float pk = (float)((1.0 + kDrawSlack) / rows.p.s), qk = with_q ? (float)((1.0 - kDrawSlack) / rows.q.s) : 0.0f;
     const E *x = row_of<E>(a, at), *d = with_q ? row_of<E>(a, a.R + drafted) : x;
     const float *noise = a.noise + b * a.ld_n;
-    const float c = a.scale, pm = pr.m, qm = with_q ? qr.m : pr.m;
-    const int64_t lo = cut * a.cut, hi = lo + a.cut < a.V ? lo + a.cut : a.V;
+    const float c = a.scale, pm = rows.p.m, qm = with_q ? rows.q.m : rows.p.m;
+    const int64_t lo64 = cut * a.cut, hi64 = lo64 + a.cut < a.V ? lo64 + a.cut : a.V;
+    const int lo = (int)lo64, hi = (int)hi64, off = threadIdx.x * kV;            // V < 2^31
     Race v{0.0f, 0.0f, -1};
-    for (int64_t col = lo + threadIdx.x * kV; col < hi; col += kBlock * kV) {
-        float xs[kV], ds[kV], ns[kV];
-        const int64_t n = hi - col;
-        load_logits(x + col, n, xs);
-        load_logits(d + col, n, ds);
-        if (n >= kV) {
+    auto race = [&](auto two) {
+        constexpr bool kTwo = decltype(two)::value;      // w = p - q
+        auto offer = [&](const float *xs, const float *ds, const float *ns, int col) {
 #pragma unroll
-            for (int i = 0; i < kV; i += 4) Elem<float>::unpack(load16(noise + col + i), ns + i);
-        } else {
-            load_head<kV>(noise + col, (int)n, 1.0f, ns);
-        }
+            for (int i = 0; i < kV; ++i) {
+                float w = __builtin_amdgcn_exp2f((xs[i] - pm) * c) * pk;
+                if constexpr (kTwo) w = __builtin_fmaxf(w - __builtin_amdgcn_exp2f((ds[i] - qm) * c) * qk, 0.0f);
+                float t = w * __builtin_amdgcn_rcpf(ns[i]);
+                if constexpr (!kTwo) t = col + i == taken ? 0.0f : t;
+                const bool first = t > v.best;
+                v.second = __builtin_fmaxf(v.second, first ? v.best : t);
+                v.best = first ? t : v.best;
+                v.column = first ? col + i : v.column;
+            }
+        };
+        int base = lo;
+        auto steps = [&](auto ahead) {                   // that many loads of each kind in flight
+            constexpr int kAhead = decltype(ahead)::value;
+            for (; hi - base >= kAhead * kStep; base += kAhead * kStep) {
+                const int col = base + off;
+                v4u xr[kAhead], dr[kAhead], nr[kAhead][kV / 4];
 #pragma unroll
-        for (int i = 0; i < kV; ++i) {
-            const float p = __builtin_amdgcn_exp2f((xs[i] - pm) * c) * pk;
-            const float q = __builtin_amdgcn_exp2f((ds[i] - qm) * c) * qk;
-            float t = __builtin_fmaxf(p - q, 0.0f) * __builtin_amdgcn_rcpf(ns[i]);
-            t = col + i == taken ? 0.0f : t;
-            const bool first = t > v.best;
-            v.second = __builtin_fmaxf(v.second, first ? v.best : t);
-            v.best = first ? t : v.best;
-            v.column = first ? col + i : v.column;
+                for (int u = 0; u < kAhead; ++u) {
+                    xr[u] = load16(x + col + u * kStep);
+                    if constexpr (kTwo) dr[u] = load16(d + col + u * kStep);
+#pragma unroll
+                    for (int i = 0; i < kV; i += 4) nr[u][i / 4] = load16(noise + col + u * kStep + i);
+                }
+#pragma unroll
+                for (int u = 0; u < kAhead; ++u) {
+                    float xs[kV], ds[kV], ns[kV];
+                    Elem<E>::unpack(xr[u], xs);
+                    if constexpr (kTwo) Elem<E>::unpack(dr[u], ds);
+#pragma unroll
+                    for (int i = 0; i < kV; i += 4) Elem<float>::unpack(nr[u][i / 4], ns + i);
+                    offer(xs, ds, ns, col + u * kStep);
+                }
+            }
+        };
+        steps(std::integral_constant<int, 2>());
+        steps(std::integral_constant<int, 1>());
+        if (hi - base > off) {                           // less than a step is left
+            float xs[kV], ds[kV], ns[kV];
+            const int col = base + off, n = hi - col;
+            load_logits(x + col, n, xs);
+            if constexpr (kTwo) load_logits(d + col, n, ds);
+            if (n >= kV) {
+#pragma unroll
+                for (int i = 0; i < kV; i += 4) Elem<float>::unpack(load16(noise + col + i), ns + i);
+            } else {
+                load_head<kV>(noise + col, n, 1.0f, ns);
+            }
+            offer(xs, ds, ns, col);
         }
-    }
+    };
+    if (with_q) race(std::true_type());
+    else race(std::false_type());
     v = merge_lanes(v);
     if (lane == 0) races[wave] = v;
     __syncthreads();
     if (threadIdx.x != 0) return;
-    for (int i = 1; i < kWaves; ++i) merge(v, races[i]);
+    for (int i = 1; i < kBlock / 64; ++i) merge(v, races[i]);
     races_of(a)[blockIdx.x] = v;
 }
 
 // ---------------------------------------------------------------- fp64
 
 constexpr int kWide = 1024;         // threads of finish
+constexpr int kWaves = kWide / 64;
 
-__device__ __forceinline__ double sum_block(double v, double (&room)[kWide / 64]) {
+__device__ __forceinline__ double sum_block(double v, double (&room)[kWaves]) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    v = sum_lanes(v);
+    v = sum_lanes<64>(v);
     if (lane == 0) room[wave] = v;
     __syncthreads();
     v = 0.0;
-    for (int i = 0; i < kWide / 64; ++i) v += room[i];
+    for (int i = 0; i < kWaves; ++i) v += room[i];
     __syncthreads();
     return v;
 }
 
+// kBatch values of a row in flight for a thread
+constexpr int kBatch = 8;
+template <class E>
+__device__ __forceinline__ void load_batch(const E *x, int64_t col0, int64_t V, float (&v)[kBatch]) {
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+        const int64_t col = col0 + k * kWide;
+        v[k] = Elem<E>::get(x[col < V ? col : 0]);
+    }
+}
+
 // A row's sum in fp64 over the same maximum
 template <class E>
-__device__ __forceinline__ RowSum exact_row(const DraftArgs &a, int64_t i, const RowSum &fast, double (&room)[kWide / 64]) {
+__device__ __forceinline__ RowSum exact_row(const DraftArgs &a, int64_t i, const RowSum &fast, double (&room)[kWaves]) {
     const E *x = row_of<E>(a, i);
     double s = 0.0;
-    for (int64_t col = threadIdx.x; col < a.V; col += kWide) s += exp2(((double)Elem<E>::get(x[col]) - fast.m) * a.scale64);
+    for (int64_t col0 = threadIdx.x; col0 < a.V; col0 += kWide * kBatch) {
+        float v[kBatch];
+        load_batch(x, col0, a.V, v);
+#pragma unroll 1
+        for (int k = 0; k < kBatch; ++k)
+            if (col0 + k * kWide < a.V) s += exp2(((double)v[k] - fast.m) * a.scale64);
+    }
     s = sum_block(s, room);
     return {fast.m, fast.s == fast.s ? s : fast.s};
 }
@@ -318,94 +426,125 @@ __device__ __forceinline__ void better(Exact &v, const Exact &o) {
 // The race in fp64: w = p - q, or p without q (`taken`: that column is left out)
 template <class E>
 __device__ __forceinline__ int64_t exact_race(const DraftArgs &a, int64_t b, int64_t at, const RowSum &pr, int64_t q_at,
-                                              const RowSum &qr, int64_t taken, Exact (&room)[kWide / 64]) {
+                                              const RowSum &qr, int64_t taken, Exact (&room)[kWaves]) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const E *x = row_of<E>(a, at), *d = q_at < 0 ? x : row_of<E>(a, q_at);
     Exact v{0.0, -1};
-    for (int64_t col = threadIdx.x; col < a.V; col += kWide) {
-        double w = share(a, Elem<E>::get(x[col]), pr);
-        if (q_at >= 0) w -= share(a, Elem<E>::get(d[col]), qr);
-        const double score = w / (double)a.noise[b * a.ld_n + col];
-        if (w > 0.0 && score > 0.0 && col != taken) better(v, Exact{score, col});
+    for (int64_t col0 = threadIdx.x; col0 < a.V; col0 += kWide * kBatch) {
+        float xs[kBatch], ds[kBatch], ns[kBatch];
+        load_batch(x, col0, a.V, xs);
+        load_batch(d, col0, a.V, ds);
+        load_batch(a.noise + b * a.ld_n, col0, a.V, ns);
+#pragma unroll 1
+        for (int k = 0; k < kBatch; ++k) {
+            const int64_t col = col0 + k * kWide;
+            double w = share(a, xs[k], pr);
+            if (q_at >= 0) w -= share(a, ds[k], qr);
+            const double score = w / (double)ns[k];
+            if (w > 0.0 && score > 0.0 && col != taken && col < a.V) better(v, Exact{score, col});
+        }
     }
 #pragma unroll
     for (int n = 1; n < 64; n <<= 1) better(v, Exact{__shfl_xor(v.score, n, 64), __shfl_xor(v.column, n, 64)});
     if (lane == 0) room[wave] = v;
     __syncthreads();
     v = room[0];
-    for (int i = 1; i < kWide / 64; ++i) better(v, room[i]);
+    for (int i = 1; i < kWaves; ++i) better(v, room[i]);
     __syncthreads();
     return v.column;
 }
 
-// One block a request
+// The token after the drafted ones, in fp64: of p - q (q_at < 0: of p without
+// the column `taken`), or of p where that is nowhere above 0.
+template <class E>
+__device__ __forceinline__ int64_t exact_draw(const DraftArgs &a, int64_t b, int64_t at, const Pair &fast, int64_t q_at, bool refused,
+                                              int64_t taken, double (&sums)[kWaves], Exact (&exacts)[kWaves]) {
+    if (fast.p.s != fast.p.s) return -1;                 // a row without a distribution
+    const RowSum p = exact_row<E>(a, at, fast.p, sums);
+    RowSum q = fast.q;
+    if (q_at >= 0) q = exact_row<E>(a, q_at, q, sums);
+    int64_t token = exact_race<E>(a, b, at, p, q_at, q, taken, exacts);
+    if (token < 0 && refused) token = exact_race<E>(a, b, at, p, -1, q, -1, exacts);
+    return token;
+}
+
+template <class E>
+__device__ __forceinline__ void put_token(const DraftArgs &a, int64_t b, int64_t at, int end, int64_t token, const RowSum &p) {
+    a.accepted[b] = end;
+    a.tokens[at] = token;
+    a.logprobs[at] = token >= 0 ? log_share(a, Elem<E>::get(row_of<E>(a, at)[token]), p) : __builtin_nanf("");
+}
+
+// A request whose decisions the fast sums leave open, or with more drafted
+// tokens than are held: one after another, the close ones in fp64, and the race
+// in fp64.
+template <class E>
+__device__ __forceinline__ void resolve(const DraftArgs &a, const Request &r, int64_t b, double (&sums)[kWaves], Exact (&exacts)[kWaves]) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    int end = 0;
+    for (; end < r.drafts; ++end) {
+        Pair rows;
+        Stand s = fast_stand<E>(a, r, end, lane, rows);
+        if (s.close) {
+            rows.p = exact_row<E>(a, r.first + end, rows.p, sums);
+            if (a.d) rows.q = exact_row<E>(a, a.R + r.draft + end, rows.q, sums);
+            s = stand_of<E>(a, r, end, s.id, a.u[r.draft + end], rows);
+        }
+        if (!s.stands) break;
+    }
+    const bool refused = end < r.drafts;
+    const int64_t q_at = refused && a.d ? a.R + r.draft + end : -1;
+    const Pair rows = join_rows(a, r.first + end, q_at, lane);
+    const int64_t token = exact_draw<E>(a, b, r.first + end, rows, q_at, refused, refused && !a.d ? a.ids[r.draft + end] : -1, sums, exacts);
+    if (threadIdx.x == 0) put_token<E>(a, b, r.first + end, end, token, rows.p);
+    for (int i = wave; i <= r.drafts; i += kWaves) {
+        if (i == end) continue;
+        int64_t id = -1;
+        float logprob = 0.0f;
+        if (i < end) {
+            Pair at;
+            const Stand s = fast_stand<E>(a, r, i, lane, at);
+            id = s.id, logprob = s.logprob;
+        }
+        if (lane == 0) a.tokens[r.first + i] = id, a.logprobs[r.first + i] = logprob;
+    }
+}
+
+// One block a request; all of its waves take the same decisions.
 template <class E>
 __global__ __launch_bounds__(kWide) void draft_finish_kernel(const DraftArgs a) {
-    __shared__ int found[2];
-    __shared__ double sums[kWide / 64];
-    __shared__ Exact exacts[kWide / 64];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    __shared__ double sums[kWaves];
+    __shared__ Exact exacts[kWaves];
+    const int lane = threadIdx.x & 63;
     const int64_t b = blockIdx.x;
     const Request r = request_of(a, b);
     if (r.drafts < 0) {
         if (threadIdx.x == 0) a.accepted[b] = 0;
         return;
     }
-    Stop stop = stop_of<E, kWide>(a, r, found);
-    if (stop.close) {                                    // one after another, the close ones in fp64
-        for (stop.end = 0; stop.end < r.drafts; ++stop.end) {
-            const int64_t row = r.first + stop.end, drafted = r.draft + stop.end;
-            RowSum p = join_row(a, row, lane), q{0.0f, 1.0};
-            if (a.d) q = join_row(a, a.R + drafted, lane);
-            Stand s = stand_of<E>(a, r, stop.end, p, q);
-            if (s.close) {
-                p = exact_row<E>(a, row, p, sums);
-                if (a.d) q = exact_row<E>(a, a.R + drafted, q, sums);
-                s = stand_of<E>(a, r, stop.end, p, q);
-            }
-            if (!s.stands) break;
-        }
+    const Verdict verdict = verdicts_of(a)[b];
+    Race v{0.0f, 0.0f, -1};
+    for (int i = lane; i < a.cuts; i += 64) merge(v, races_of(a)[b * a.cuts + i]);
+    if (verdict.open) {
+        resolve<E>(a, r, b, sums, exacts);
+        return;
     }
-    const int64_t at = r.first + stop.end, drafted = r.draft + stop.end;
-    const bool refused = stop.end < r.drafts, with_q = refused && a.d;
-    RowSum pr = join_row(a, at, lane), qr{0.0f, 1.0};
-    const RowSum fast = pr;
-    if (with_q) qr = join_row(a, a.R + drafted, lane);
-    const int64_t taken = refused && !a.d ? a.ids[drafted] : -1;
+    v = merge_lanes(v);
+    const Pair &rows = verdict.rows;
+    const int64_t at = r.first + verdict.end, drafted = r.draft + verdict.end;
+    const bool refused = verdict.end < r.drafts;
+    const int64_t q_at = refused && a.d ? a.R + drafted : -1;
     int64_t token = -1;
-    if (pr.s == pr.s) {                                  // the row has a distribution
-        bool certain = false;
-        if (!stop.close) {
-            Race v{0.0f, 0.0f, -1};
-            for (int i = lane; i < a.cuts; i += 64) merge(v, races_of(a)[b * a.cuts + i]);
-            v = merge_lanes(v);
-            if (v.column >= 0) {
-                const double p = share(a, Elem<E>::get(row_of<E>(a, at)[v.column]), pr);
-                const double q = with_q ? share(a, Elem<E>::get(row_of<E>(a, a.R + drafted)[v.column]), qr) : 0.0;
-                const double lower = ((1.0 - kDrawSlack) * p - (1.0 + kDrawSlack) * q) / (double)a.noise[b * a.ld_n + v.column];
-                certain = (double)v.second < lower;
-                token = v.column;
-            }
-        }
-        if (!certain) {                                  // uniform: every wave has joined the same races
-            pr = exact_row<E>(a, at, pr, sums);
-            if (with_q) qr = exact_row<E>(a, a.R + drafted, qr, sums);
-            token = exact_race<E>(a, b, at, pr, with_q ? a.R + drafted : -1, qr, taken, exacts);
-            if (token < 0 && refused) token = exact_race<E>(a, b, at, pr, -1, qr, -1, exacts);
-        }
+    bool certain = !(rows.p.s == rows.p.s);              // a row without a distribution has no token
+    if (!certain && v.column >= 0) {
+        const double p = share(a, Elem<E>::get(row_of<E>(a, at)[v.column]), rows.p);
+        const double q = q_at >= 0 ? share(a, Elem<E>::get(row_of<E>(a, q_at)[v.column]), rows.q) : 0.0;
+        const double lower = ((1.0 - kDrawSlack) * p - (1.0 + kDrawSlack) * q) / (double)a.noise[b * a.ld_n + v.column];
+        certain = (double)v.second < lower;
+        token = v.column;
     }
-    if (threadIdx.x == 0) a.accepted[b] = stop.end;
-    for (int i = wave; i <= r.drafts; i += kWide / 64) {
-        const int64_t row = r.first + i;
-        const int64_t id = i < stop.end ? a.ids[r.draft + i] : i == stop.end ? token : -1;
-        const RowSum p = i < stop.end ? join_row(a, row, lane) : fast;
-        if (lane == 0) {
-            float logp = i == stop.end ? __builtin_nanf("") : 0.0f;
-            if (id >= 0) logp = (float)(((double)Elem<E>::get(row_of<E>(a, row)[id]) - p.m) * a.inv_temperature - log(p.s));
-            a.tokens[row] = id;
-            a.logprobs[row] = logp;
-        }
-    }
+    if (!certain) token = exact_draw<E>(a, b, at, rows, q_at, refused, refused && !a.d ? a.ids[drafted] : -1, sums, exacts);
+    if (threadIdx.x == 0) put_token<E>(a, b, at, verdict.end, token, rows.p);
 }
 
 template <class E, bool ONCE>
@@ -431,11 +570,11 @@ DraftCut draft_cut(int64_t rows, int64_t B, int64_t V, int cus) {
         const int64_t want = ceil_div((int64_t)cus * 4, rows), most = ceil_div(V, 4096);
         slices = want < most ? want : most;
     }
-    // cuts of a race: four blocks for every compute unit, of at least 2048 columns
-    const int64_t want = ceil_div((int64_t)cus * 4, B), most = ceil_div(V, 2048);
+    // cuts of a race: as many blocks as are resident at once, of at least 2048 columns
+    const int64_t want = B < kDrawBlocks * (int64_t)cus ? kDrawBlocks * (int64_t)cus / B : 1, most = ceil_div(V, 2048);
     const int64_t cuts = want < most ? want : most;
     return {(int)slices, (int)cuts, ceil_div(ceil_div(V, slices), 8) * 8, ceil_div(ceil_div(V, cuts), 8) * 8,
-            rows * slices * (int64_t)sizeof(Part) + B * cuts * (int64_t)sizeof(Race)};
+            rows * slices * (int64_t)sizeof(Part) + B * ((int64_t)sizeof(Verdict) + cuts * (int64_t)sizeof(Race))};
 }
 
 hipError_t launch_drafts(DraftArgs a, bool bf16, hipStream_t stream) {

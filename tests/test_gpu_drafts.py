@@ -120,7 +120,7 @@ def test_against_the_rule(mx, which, V, dtype):
             _check(mx, *_case(COUNTS[which], V, dtype, 100 * which + V % 97, draft, t), temperature=t)
 
 
-@pytest.mark.parametrize("counts,V", [([4], 131072), ([3, 0, 5, 1], 100003), ([2] * 300, 1000), ([1] * 700, 999), ([5] * 30, 70001)])
+@pytest.mark.parametrize("counts,V", [([40, 2, 31, 32], 300), ([100], 5000), ([4], 131072), ([3, 0, 5, 1], 100003), ([2] * 300, 1000), ([1] * 700, 999), ([5] * 30, 70001)])
 def test_larger(mx, counts, V):
     for dtype in (torch.float32, torch.bfloat16):
         _check(mx, *_case(counts, V, dtype, V % 1000))
