@@ -51,7 +51,7 @@ struct Parts {
 struct LoraBackwardParts {
     LoraCut cut;
     LoraOuterPlan plan;
-    int64_t at, bt, part, s, slots_a, slots_b, total;
+    int64_t at, bt, part, s, h, slots_a, slots_b, total;
 };
 LoraBackwardParts lora_backward_parts(int64_t rows, int64_t E, int64_t r, int64_t K, int64_t N) {
     LoraBackwardParts w{};
@@ -60,7 +60,8 @@ LoraBackwardParts lora_backward_parts(int64_t rows, int64_t E, int64_t r, int64_
     w.plan = lora_outer_plan(rows, E, r, K, N, cus);
     Parts p;
     w.at = p.take(E * r * K * 2), w.bt = p.take(E * r * N * 2);
-    w.part = p.take(w.cut.splits * rows * r * 4), w.s = p.take(rows * r * 4);
+    w.part = p.take(w.cut.splits * rows * r * 4);
+    w.s = p.take(lora_packed_bytes(rows, r)), w.h = p.take(lora_packed_bytes(rows, r));
     w.slots_a = p.take(w.plan.slots * r * K * 4), w.slots_b = p.take(w.plan.slots * r * N * 4);
     w.total = p.at;
     return w;
@@ -188,13 +189,14 @@ mxfp8_status mxfp8_lora_backward(void *d_x, int64_t ld_dx, const void *d_y, int6
     mxfp8_status st = check_device();
     if (st != MXFP8_OK) return st;
     char *base = static_cast<char *>(workspace);
-    float *s_rows = reinterpret_cast<float *>(base + w.s);
+    LoraVec *s_rows = reinterpret_cast<LoraVec *>(base + w.s), *h_rows = reinterpret_cast<LoraVec *>(base + w.h);
     if (used) {
-        LoraTranspose t{};
-        t.E = (int)E;
+        LoraPrepare t{};
+        t.hidden = hidden, t.packed = h_rows, t.scales = scales, t.offsets = offsets, t.row_token = row_token;
+        t.rows = rows, t.T = T, t.E = (int)E, t.r = (int)r;
         t.job[0] = {static_cast<const uint16_t *>(a), reinterpret_cast<uint16_t *>(base + w.at), (int)r, (int)K};
         t.job[1] = {static_cast<const uint16_t *>(b), reinterpret_cast<uint16_t *>(base + w.bt), (int)N, (int)r};
-        st = finish(launch_lora_transpose(t, stream));
+        st = finish(launch_lora_prepare(t, stream));
         if (st != MXFP8_OK) return st;
         LoraShrink s{};
         s.x = static_cast<const uint16_t *>(d_y), s.ld = ld_dy, s.T = T, s.w = t.job[1].to, s.offsets = offsets;
@@ -204,15 +206,15 @@ mxfp8_status mxfp8_lora_backward(void *d_x, int64_t ld_dx, const void *d_y, int6
         if (st != MXFP8_OK) return st;
         LoraExpand p{};
         p.y = d_x, p.ld = ld_dx, p.T = T, p.w = t.job[0].to, p.scales = scales, p.offsets = offsets;
-        p.row_token = row_token, p.rows = rows, p.part = s.part, p.hidden = s_rows;
+        p.row_token = row_token, p.rows = rows, p.part = s.part, p.packed = s_rows;
         p.E = (int)E, p.r = (int)r, p.N = d_x ? (int)K : 0, p.splits = w.cut.splits;
         st = finish(launch_lora_expand(p, true, stream));
         if (st != MXFP8_OK) return st;
     }
     LoraOuter o{};
     o.wide[0] = {s_rows, x, x_s, grid ? K : ld_x, packed_ksteps(K), (int)K, d_a, reinterpret_cast<float *>(base + w.slots_a), 0};
-    o.wide[1] = {hidden, d_y, nullptr, ld_dy, 0, (int)N, d_b, reinterpret_cast<float *>(base + w.slots_b), 0};
-    o.scales = scales, o.offsets = offsets, o.row_token = row_token, o.rows = used, o.T = T, o.E = (int)E, o.r = (int)r;
+    o.wide[1] = {h_rows, d_y, nullptr, ld_dy, 0, (int)N, d_b, reinterpret_cast<float *>(base + w.slots_b), 0};
+    o.offsets = offsets, o.row_token = row_token, o.rows = used, o.T = T, o.E = (int)E, o.r = (int)r;
     return finish(launch_lora_outer(o, w.plan, form, stream));
 }
 

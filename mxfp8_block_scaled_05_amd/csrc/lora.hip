@@ -53,6 +53,10 @@ __device__ __forceinline__ void split_pair(float v0, float v1, uint32_t (&out)[N
     }
 }
 
+// The compiler moves a load to where its value is first used, a round later,
+// unless it must not.
+__device__ __forceinline__ void keep_order() { asm volatile("" ::: "memory"); }
+
 // The number of offsets[0..E] that are at most row, less one: the group that
 // the row lies in (-1 or E: none).  All lanes of the wave take part.
 __device__ __forceinline__ int adapter_of(const int32_t *offsets, int E, int row, int lane) {
@@ -175,6 +179,7 @@ __global__ __launch_bounds__(kBlock) void lora_shrink_kernel(const LoraShrink a)
         for (; k0 + S::kChunk <= k1; k0 += kStep) {
             turn();
             ask(k0 + kStep + S::kChunk <= k1 ? k0 + kStep : k0);         // the last time for nothing
+            keep_order();
             use();
         }
     }
@@ -201,6 +206,22 @@ __global__ __launch_bounds__(kBlock) void lora_shrink_kernel(const LoraShrink a)
         if (token_of(a.row_token, (int64_t)rb * kRows + row, a.T) < 0) v = v4f{0, 0, 0, 0};
         *reinterpret_cast<v4f *>(out + (int64_t)row * a.r + q * 4) = v;
     }
+}
+
+// P as the outer products take it: for every 32 rows and 16 ranks three
+// fragments, a lane's 8 rows of one rank, 1 KB each.
+constexpr int kOuterParts = 3;
+__device__ __forceinline__ void pack_rows(const float (&p)[8], v4u *out) {
+    v4u parts[kOuterParts];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        uint32_t word[kOuterParts];
+        split_pair(p[2 * q], p[2 * q + 1], word);
+#pragma unroll
+        for (int n = 0; n < kOuterParts; ++n) parts[n][q] = word[n];
+    }
+#pragma unroll
+    for (int n = 0; n < kOuterParts; ++n) out[n * 64] = parts[n];
 }
 
 // ---------------------------------------------------------------- expand
@@ -240,6 +261,10 @@ __global__ __launch_bounds__(kBlock, KT == 4 ? 1 : 2) void lora_expand_kernel(co
     constexpr bool kTurnB = KT > 1;
     constexpr int kB = 4 * KT;                           // 16-byte pieces of a row of B, and of a lane's B
     __shared__ v4u bs[kTurnB ? kWaves * 64 * kB : 1];
+    // scaled P of the block's rows, first 64 ranks and the rest, before what `turn` and `bs` are for
+    auto flat = reinterpret_cast<float (*)[68]>(&turn[0][0][0]);
+    auto upper = reinterpret_cast<float (*)[68]>(&bs[0]);
+    static_assert(RB * 32 * 68 * 4 <= sizeof(turn) && (KT < 4 || RB * 32 * 68 * 4 <= sizeof(bs)), "P's rows fit");
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int m = lane & 15, kg = lane >> 4;
     const int group = blockIdx.x / a.step, tile0 = blockIdx.x - group * a.step;
@@ -274,10 +299,15 @@ __global__ __launch_bounds__(kBlock, KT == 4 ? 1 : 2) void lora_expand_kernel(co
             const int at = i < per ? i * 64 + lane : lane;               // pieces that there are not: the first again
             b_piece[i] = at;
             b_slot[i] = slot(at / per, at % per);
-            mine[i * 64 + lane] = v4u{0, 0, 0, 0};       // ranks past r
         }
-        wave_sync();
     }
+    auto clear_b = [&]() {                               // ranks past r
+        if constexpr (kTurnB) {
+#pragma unroll
+            for (int i = 0; i < kB; ++i) mine[i * 64 + lane] = v4u{0, 0, 0, 0};
+            wave_sync();
+        }
+    };
     // All 64 rows have a token, one adapter and whole columns: nothing is branched around, so that the compiler counts
     // what is in flight and waits for the oldest alone.  Otherwise rows of padding and columns past N are loaded from
     // row 0 and column 0 and not stored.
@@ -365,10 +395,12 @@ __global__ __launch_bounds__(kBlock, KT == 4 ? 1 : 2) void lora_expand_kernel(co
             for (; c0 < a.N; c0 += 2 * step) {
                 turn_b();
                 ask(n[1], adapter, c0 + step < a.N ? c0 + step : c0);    // the last time for nothing
+                keep_order();
                 use(whole_rows, n[0], adapter, c0);
                 if (c0 + step >= a.N) break;
                 turn_b();
                 ask(n[0], adapter, c0 + 2 * step < a.N ? c0 + 2 * step : c0 + step);
+                keep_order();
                 use(whole_rows, n[1], adapter, c0 + step);
             }
         }
@@ -412,8 +444,35 @@ __global__ __launch_bounds__(kBlock, KT == 4 ? 1 : 2) void lora_expand_kernel(co
         }
 #pragma unroll
         for (int n = 0; n < kParts; ++n) frag[mt][kt][n][l] = parts[n];
+        if (a.packed && tile0 == 0) {                    // for the outer products below, by way of LDS; half of rank 128 at a time
+#pragma unroll
+            for (int q = 0; q < 8; ++q) v[q] = ee >= 0 ? v[q] * scale : 0.0f;
+            if (j < 64) {
+                *reinterpret_cast<v4f *>(&flat[mt * 16 + (l & 15)][j]) = v4f{v[0], v[1], v[2], v[3]};
+                *reinterpret_cast<v4f *>(&flat[mt * 16 + (l & 15)][j + 4]) = v4f{v[4], v[5], v[6], v[7]};
+            } else {
+                *reinterpret_cast<v4f *>(&upper[mt * 16 + (l & 15)][j - 64]) = v4f{v[0], v[1], v[2], v[3]};
+                *reinterpret_cast<v4f *>(&upper[mt * 16 + (l & 15)][j - 60]) = v4f{v[4], v[5], v[6], v[7]};
+            }
+        }
     }
     __syncthreads();
+    if (a.packed && tile0 == 0) {
+        const int tiles = (a.r + 15) / 16;
+        for (int i = wave; i < RB * tiles; i += kWaves) {
+            const int rb = rb0 + i / tiles, jt = i % tiles;
+            if (rb >= blocks) break;
+            float p[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                const int row = (rb - rb0) * kRows + kg * 8 + q;
+                p[q] = jt < 4 ? flat[row][jt * 16 + m] : upper[row][jt * 16 - 64 + m];
+            }
+            pack_rows(p, a.packed + ((int64_t)rb * tiles + jt) * kOuterParts * 64 + lane);
+        }
+        __syncthreads();
+    }
+    clear_b();
     // groups of one adapter together, one after another where they differ
 #pragma unroll
     for (int s = 0; s < RB; ++s) {
@@ -425,12 +484,34 @@ __global__ __launch_bounds__(kBlock, KT == 4 ? 1 : 2) void lora_expand_kernel(co
     }
 }
 
-// ---------------------------------------------------------------- transposed weights
+// ---------------------------------------------------------------- before the gradients
 
-// [E][P][Q] -> [E][Q][P], 64 x 64 tiles, P and Q multiples of 8
-__global__ __launch_bounds__(kBlock) void lora_transpose_kernel(const LoraTranspose a) {
+// The weights transposed, [E][P][Q] -> [E][Q][P] in 64 x 64 tiles (P and Q
+// multiples of 8), and the hidden rows, scaled, as the outer products take them.
+__global__ __launch_bounds__(kBlock) void lora_prepare_kernel(const LoraPrepare a) {
     __shared__ uint16_t t[64][72];
-    const LoraTranspose::Job &job = a.job[blockIdx.y];
+    if (blockIdx.y == 2) {
+        const int lane = threadIdx.x & 63, m = lane & 15, kg = lane >> 4;
+        const int tiles = (a.r + 15) / 16;
+        const int64_t all = a.rows / kRows * tiles;
+        for (int64_t i = (int64_t)blockIdx.x * kWaves + (threadIdx.x >> 6); i < all; i += (int64_t)gridDim.x * kWaves) {
+            const int64_t rb = i / tiles;
+            const int rank = (int)(i - rb * tiles) * 16 + m;
+            const int e = adapter_of(a.offsets, a.E, (int)rb * kRows, lane);
+            const bool in = e >= 0 && e < a.E && rank < a.r;
+            const float scale = in && a.scales ? a.scales[e] : 1.0f;
+            float p[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                const int64_t row = rb * kRows + kg * 8 + q;
+                const float v = a.hidden[row * a.r + (rank < a.r ? rank : 0)];
+                p[q] = in && token_of(a.row_token, row, a.T) >= 0 ? v * scale : 0.0f;
+            }
+            pack_rows(p, a.packed + i * kOuterParts * 64 + lane);
+        }
+        return;
+    }
+    const LoraPrepare::Job &job = a.job[blockIdx.y];
     const int across = (job.Q + 63) / 64, down = (job.P + 63) / 64;
     for (int64_t at = blockIdx.x; at < (int64_t)a.E * across * down; at += gridDim.x) {
         const int64_t e = at / (across * down);
@@ -521,15 +602,22 @@ __device__ __forceinline__ Item item_of(const LoraOuter &a, int item, int lane) 
 // The columns at `col` exist where `in`.
 __device__ __forceinline__ uint32_t low_halves(uint32_t a, uint32_t b) { return __builtin_amdgcn_perm(b, a, 0x05040100u); }
 __device__ __forceinline__ uint32_t high_halves(uint32_t a, uint32_t b) { return __builtin_amdgcn_perm(b, a, 0x07060302u); }
+// load() only asks: what is done with the values waits for settle().
 struct WideBf16 {
     v4u r[8];
+    uint32_t real;                                       // bit i: row i has a token
     __device__ __forceinline__ void load(const LoraWide &w, const int *token, int col, bool in) {
+        real = 0;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const bool real = token[i] >= 0 && in;
-            const v4u v = *reinterpret_cast<const v4u *>(static_cast<const uint16_t *>(w.x) + (real ? token[i] * w.ld + col : 0));
-            r[i] = real ? v : v4u{0, 0, 0, 0};
+            const bool has = token[i] >= 0 && in;
+            real |= has ? 1u << i : 0u;
+            r[i] = *reinterpret_cast<const v4u *>(static_cast<const uint16_t *>(w.x) + (has ? token[i] * w.ld + col : 0));
         }
+    }
+    __device__ __forceinline__ void settle() {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) r[i] = real >> i & 1 ? r[i] : v4u{0, 0, 0, 0};
     }
     __device__ __forceinline__ v4u column(int c) const {
         v4u f;
@@ -545,13 +633,16 @@ struct WideBf16 {
 template <bool PACKED>
 struct WideGrid {
     v2i q[8];
+    uint8_t code[8];
     float scale[8];
+    uint32_t real;
     __device__ __forceinline__ void load(const LoraWide &w, const int *token, int col, bool in) {
         const uint8_t *x = static_cast<const uint8_t *>(w.x);
+        real = 0;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const bool real = token[i] >= 0 && in;
-            const int t = real ? token[i] : 0, c = real ? col : 0;
+            const bool has = token[i] >= 0 && in;
+            const int t = has ? token[i] : 0, c = has ? col : 0;
             int64_t at, sat;
             if constexpr (PACKED) {
                 const int64_t tile = (int64_t)(t >> 8) * w.ksteps + (c >> 7);
@@ -562,11 +653,18 @@ struct WideGrid {
                 at = t * w.ld + c;
                 sat = t * (w.ld >> 5) + (c >> 5);
             }
-            const v2i v = *reinterpret_cast<const v2i *>(x + at);
-            const uint32_t code = w.s[sat];
-            q[i] = real ? v : v2i{0, 0};
-            scale[i] = bits_to_float(code == 0u ? 0x00400000u : code == 255u ? 0x7FC00000u : code << 23);
-            if (!real) scale[i] = 0.0f;
+            real |= has ? 1u << i : 0u;
+            q[i] = *reinterpret_cast<const v2i *>(x + at);
+            code[i] = w.s[sat];
+        }
+    }
+    __device__ __forceinline__ void settle() {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t c = code[i];
+            const bool has = real >> i & 1;
+            q[i] = has ? q[i] : v2i{0, 0};
+            scale[i] = bits_to_float(!has ? 0u : c == 0u ? 0x00400000u : c == 255u ? 0x7FC00000u : c << 23);
         }
     }
     __device__ __forceinline__ float value(int i, int c) const {
@@ -582,12 +680,10 @@ struct WideGrid {
     }
 };
 
-constexpr int kOuterParts = 3;
-
 template <int RT, class Wide>
-__device__ __forceinline__ void outer_rows(const LoraOuter &a, const LoraWide &w, const Item &it, float scale, int j0, int col,
-                                           bool in, int lane, int wave, v4f (&acc)[RT][8]) {
-    const int m = lane & 15, kg = lane >> 4;
+__device__ __forceinline__ void outer_rows(const LoraOuter &a, const LoraWide &w, const Item &it, int jt0, int col, bool in, int lane,
+                                           int wave, v4f (&acc)[RT][8]) {
+    const int kg = lane >> 4, tiles = (a.r + 15) / 16;
     constexpr int kStep = kWaves * kRows;
     // While a block of 32 rows is used, the next one's values and the tokens of the one after it are on their way.
     int64_t named[8];
@@ -595,40 +691,29 @@ __device__ __forceinline__ void outer_rows(const LoraOuter &a, const LoraWide &w
 #pragma unroll
         for (int i = 0; i < 8; ++i) named[i] = a.row_token[row < it.row1 ? row + kg * 8 + i : 0];
     };
-    auto ask = [&](int row, Wide &x, int (&token)[8]) {
+    auto take_tokens = [&](int row, int (&token)[8]) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) token[i] = named[i] >= 0 && named[i] < a.T && row < it.row1 ? (int)named[i] : -1;
-        x.load(w, token, col, in);
     };
-    auto use = [&](int row, const Wide &x, const int (&token)[8], const float (&p)[RT][8]) {
-        v4u parts[RT][kOuterParts];
+    auto ask_p = [&](int row, v4u (&p)[RT][kOuterParts]) {
+        row = row < it.row1 ? row : it.row0;
 #pragma unroll
-        for (int j = 0; j < RT; ++j)
+        for (int j = 0; j < RT; ++j) {
+            const int jt = jt0 + j < tiles ? jt0 + j : jt0;              // ranks that there are not: not kept
+            const v4u *from = w.p + ((int64_t)(row >> 5) * tiles + jt) * kOuterParts * 64 + lane;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                // a padding row's p must not meet the zeros that stand for its x as a NaN
-                const float s0 = token[2 * q] >= 0 ? p[j][2 * q] * scale : 0.0f;
-                const float s1 = token[2 * q + 1] >= 0 ? p[j][2 * q + 1] * scale : 0.0f;
-                uint32_t word[kOuterParts];
-                split_pair(s0, s1, word);
-#pragma unroll
-                for (int n = 0; n < kOuterParts; ++n) parts[j][n][q] = word[n];
-            }
+            for (int n = 0; n < kOuterParts; ++n) p[j][n] = from[n * 64];
+        }
+    };
+    auto use = [&](Wide &x, const v4u (&p)[RT][kOuterParts]) {
+        x.settle();
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
             const v4u f = x.column(c);
 #pragma unroll
             for (int n = kOuterParts - 1; n >= 0; --n)
 #pragma unroll
-                for (int j = 0; j < RT; ++j) acc[j][c] = mfma(parts[j][n], f, acc[j][c]);
-        }
-    };
-    auto ask_p = [&](int row, float (&p)[RT][8]) {
-#pragma unroll
-        for (int j = 0; j < RT; ++j) {
-            const int rank = j0 + j * 16 + m;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) p[j][i] = w.p[(int64_t)(row + kg * 8 + i) * a.r + (rank < a.r ? rank : 0)];
+                for (int j = 0; j < RT; ++j) acc[j][c] = mfma(p[j][n], f, acc[j][c]);
         }
     };
     Wide x[2];
@@ -637,20 +722,28 @@ __device__ __forceinline__ void outer_rows(const LoraOuter &a, const LoraWide &w
     // An item without rows may belong to a call without any: nothing at all is read then.  Behind an item's last rows
     // row 0 of the tables and of x stands in for what would be next.
     if (row >= it.row1) return;
+    // Loads come back in the order of their asking, so the tokens are asked for first: the values that need them must
+    // not have to wait for the values before.
+    v4u p[2][RT][kOuterParts];
     ask_tokens(row);
-    ask(row, x[0], token[0]);
+    take_tokens(row, token[0]);
     ask_tokens(row + kStep);
+    ask_p(row, p[0]);
+    x[0].load(w, token[0], col, in);
     for (; row < it.row1; row += 2 * kStep) {
-        float p[RT][8];
-        ask_p(row, p);
-        ask(row + kStep, x[1], token[1]);
+        take_tokens(row + kStep, token[1]);
         ask_tokens(row + 2 * kStep);
-        use(row, x[0], token[0], p);
+        ask_p(row + kStep, p[1]);
+        x[1].load(w, token[1], col, in);
+        keep_order();
+        use(x[0], p[0]);
         if (row + kStep >= it.row1) break;
-        ask_p(row + kStep, p);
-        ask(row + 2 * kStep, x[0], token[0]);
+        take_tokens(row + 2 * kStep, token[0]);
         ask_tokens(row + 3 * kStep);
-        use(row + kStep, x[1], token[1], p);
+        ask_p(row + 2 * kStep, p[0]);
+        x[0].load(w, token[0], col, in);
+        keep_order();
+        use(x[1], p[1]);
     }
 }
 
@@ -665,13 +758,12 @@ __device__ __forceinline__ void outer_block(const LoraOuter &a, const Item &it, 
     const int m = lane & 15, kg = lane >> 4;
     const int col = slab * 128 + m * 8;
     const bool in = col < w.C;
-    const float scale = a.scales ? a.scales[it.e] : 1.0f;
     v4f acc[RT][8];
 #pragma unroll
     for (int j = 0; j < RT; ++j)
 #pragma unroll
         for (int c = 0; c < 8; ++c) acc[j][c] = v4f{0, 0, 0, 0};
-    outer_rows<RT, Wide>(a, w, it, scale, j0, col, in, lane, wave, acc);
+    outer_rows<RT, Wide>(a, w, it, j0 / 16, col, in, lane, wave, acc);
 
     // the four waves' sums, always in the same order: (0 + 2) + (1 + 3)
     if (wave >= 2) {
@@ -714,7 +806,7 @@ __device__ __forceinline__ void outer_block(const LoraOuter &a, const Item &it, 
 }
 
 template <int RT, class WideX>
-__global__ __launch_bounds__(kBlock) void lora_outer_kernel(const LoraOuter a) {
+__global__ __launch_bounds__(kBlock, RT <= 2 ? 2 : 1) void lora_outer_kernel(const LoraOuter a) {
     __shared__ v4u red[2][RT * 8][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int per = a.wide[0].slabs + a.wide[1].slabs;
@@ -822,14 +914,14 @@ hipError_t launch_lora_expand(LoraExpand a, bool y_bf16, hipStream_t stream) {
     return hipGetLastError();
 }
 
-hipError_t launch_lora_transpose(const LoraTranspose &a, hipStream_t stream) {
-    int64_t most = 1;
-    for (const LoraTranspose::Job &j : a.job) {
+hipError_t launch_lora_prepare(const LoraPrepare &a, hipStream_t stream) {
+    int64_t most = ceil_div(a.rows / kRows * ceil_div(a.r, 16), kWaves);
+    for (const LoraPrepare::Job &j : a.job) {
         const int64_t n = a.E * ceil_div(j.P, 64) * ceil_div(j.Q, 64);
         most = most > n ? most : n;
     }
     const int64_t cap = 8 * (int64_t)device_cu_count();
-    lora_transpose_kernel<<<dim3((unsigned)(most < cap ? most : cap), 2), kBlock, 0, stream>>>(a);
+    lora_prepare_kernel<<<dim3((unsigned)(most < cap ? most : cap), 3), kBlock, 0, stream>>>(a);
     return hipGetLastError();
 }
 

@@ -263,6 +263,7 @@ hipError_t launch_swiglu_backward(const SwigluArgs &a, hipStream_t stream);
 // Low-rank adapters (lora.hip).  rows: sorted rows, a multiple of 32.
 constexpr int kLoraMaxRank = 128;
 constexpr int kLoraMaxAdapters = 1024;
+typedef uint32_t LoraVec __attribute__((ext_vector_type(4)));
 struct LoraShrink {
     const uint16_t *x;          // [T][ld], K columns
     int64_t ld, T;
@@ -288,26 +289,35 @@ struct LoraExpand {
     int64_t rows;
     const float *part;          // [splits][rows][r]
     float *hidden;              // [rows][r] or null: the sum of the partials
+    LoraVec *packed;      // or null: lora_packed_bytes of it, scaled
     int E, r, N, splits;        // N = 0: hidden alone
     int step;                   // set by the launcher: blocks beside each other on the same rows
 };
 hipError_t launch_lora_expand(LoraExpand a, bool y_bf16, hipStream_t stream);
-struct LoraTranspose {
+struct LoraPrepare {
     struct Job {
         const uint16_t *from;   // [E][P][Q]
         uint16_t *to;           // [E][Q][P]
         int P, Q;
     } job[2];
-    int E;
+    const float *hidden;        // [rows][r]
+    LoraVec *packed;      // lora_packed_bytes of it, scaled
+    const float *scales;
+    const int32_t *offsets;
+    const int64_t *row_token;
+    int64_t rows, T;
+    int E, r;
 };
-hipError_t launch_lora_transpose(const LoraTranspose &a, hipStream_t stream);
+// rows of P as the outer products take them
+inline int64_t lora_packed_bytes(int64_t rows, int64_t r) { return rows / 32 * ((r + 15) / 16) * 3 * 1024; }
+hipError_t launch_lora_prepare(const LoraPrepare &a, hipStream_t stream);
 // sums over rows, cut into chunks: items at most, slots of partial sums at most
 struct LoraOuterPlan {
     int64_t chunk, items, slots;
 };
 LoraOuterPlan lora_outer_plan(int64_t rows, int64_t E, int64_t r, int64_t K, int64_t N, int cus);
 struct LoraWide {
-    const float *p;             // [rows][r]
+    const LoraVec *p;     // lora_packed_bytes
     const void *x;              // [T][ld] bf16, or a grid's codes
     const uint8_t *s;           // the grid's scales
     int64_t ld, ksteps;
@@ -318,7 +328,6 @@ struct LoraWide {
 };
 struct LoraOuter {
     LoraWide wide[2];           // the second is bf16
-    const float *scales;
     const int32_t *offsets;
     const int64_t *row_token;
     int64_t rows, T;
