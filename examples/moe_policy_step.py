@@ -40,7 +40,8 @@ def _token_grid(cols, rows, device):
 
 @dataclass
 class Config:
-    """Sizes in multiples of 128; choice as mx.route takes it."""
+    """Sizes in multiples of 128; choice as mx.route takes it.  checkpoint: gate | up kept in 8 bits for the backward
+    pass, which computes the experts' product again (2.06 bytes a value of it instead of 5.03)."""
     hidden: int = 1024
     inter: int = 512
     experts: int = 32
@@ -49,6 +50,7 @@ class Config:
     groups: int = 4
     groups_kept: int = 2
     scale: float = 1.0
+    checkpoint: bool = False
 
 
 class MoePolicy:
@@ -97,11 +99,15 @@ class MoePolicy:
         # rows after the last group are not written by the grouped GEMMs: they start as zeros
         gu = torch.zeros((rows, 2 * c.inter), dtype=BF16, device=dev)
         mx.grouped_gemm_packed(xq, self._grids["gate_up"][0], t.offsets, BF16, out=gu)
-        s["gu"] = gu
-        gate, up = gu.float().chunk(2, 1)
-        h = (torch.nn.functional.silu(gate) * up).to(BF16)
-        s["h0"], h1 = _token_grid(c.inter, s["rows128"], dev), _grid(1, rows, c.inter, dev)
-        mx.quantize_dual_grouped_packed_(h, t.offsets, s["offsets128"], s["h0"], h1)
+        if c.checkpoint:
+            act = mx.swiglu(gu, layout="packed")
+            h1, s["saved"] = act.h, (act.saved_q, act.saved_s)
+        else:
+            s["gu"] = gu
+            gate, up = gu.float().chunk(2, 1)
+            h = (torch.nn.functional.silu(gate) * up).to(BF16)
+            s["h0"], h1 = _token_grid(c.inter, s["rows128"], dev), _grid(1, rows, c.inter, dev)
+            mx.quantize_dual_grouped_packed_(h, t.offsets, s["offsets128"], s["h0"], h1)
         s["y"] = torch.zeros((rows, c.hidden), dtype=BF16, device=dev)
         mx.grouped_gemm_packed(h1, self._grids["down"][0], t.offsets, BF16, out=s["y"])
         hid = x + mx.moe_combine(s["y"], t.pair_row, s["w"])
@@ -130,12 +136,18 @@ class MoePolicy:
         mx.quantize_dual_grouped_packed_(d_y, t.offsets, s["offsets128"], dy0, dy1)
         d_h = torch.zeros((rows, c.inter), dtype=BF16, device=dev)
         mx.grouped_gemm_packed(dy1, self._grids["down"][1], t.offsets, BF16, out=d_h)
-        out["down"] = mx.grouped_gemm_wgrad(*dy0, *s["h0"], s["offsets128"], torch.float32)
+        if c.checkpoint:
+            d_gu, h = mx.swiglu_backward(d_h, *s["saved"])
+            h0 = _token_grid(c.inter, s["rows128"], dev)
+            mx.quantize_dual_grouped_into(h, t.offsets, s["offsets128"], *h0)
+        else:
+            h0 = s["h0"]
+            gate, up = s["gu"].float().chunk(2, 1)
+            sig = torch.sigmoid(gate)
+            d_gate = d_h.float() * up * sig * (1 + gate * (1 - sig))
+            d_gu = torch.cat((d_gate, d_h.float() * gate * sig), 1).to(BF16)
+        out["down"] = mx.grouped_gemm_wgrad(*dy0, *h0, s["offsets128"], torch.float32)
 
-        gate, up = s["gu"].float().chunk(2, 1)
-        sig = torch.sigmoid(gate)
-        d_gate = d_h.float() * up * sig * (1 + gate * (1 - sig))
-        d_gu = torch.cat((d_gate, d_h.float() * gate * sig), 1).to(BF16)
         dg0, dg1 = _token_grid(2 * c.inter, s["rows128"], dev), _grid(1, rows, 2 * c.inter, dev)
         mx.quantize_dual_grouped_packed_(d_gu, t.offsets, s["offsets128"], dg0, dg1)
         d_rows = torch.zeros((rows, c.hidden), dtype=BF16, device=dev)
