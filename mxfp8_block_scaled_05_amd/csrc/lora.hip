@@ -69,11 +69,8 @@ __device__ __forceinline__ int adapter_of(const int32_t *offsets, int E, int row
     return n - 1;
 }
 
-// The token of a sorted row, -1 for padding
-__device__ __forceinline__ int token_of(const int64_t *row_token, int64_t row, int64_t T) {
-    const int64_t t = row_token[row];
-    return t >= 0 && t < T ? (int)t : -1;
-}
+// The token that a row's entry names, -1 for padding
+__device__ __forceinline__ int token_of(int64_t t, int64_t T) { return t >= 0 && t < T ? (int)t : -1; }
 
 // ---------------------------------------------------------------- shrink
 
@@ -104,15 +101,18 @@ __global__ __launch_bounds__(kBlock) void lora_shrink_kernel(const LoraShrink a)
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int m = lane & 15, kg = lane >> 4;
     const int rb = blockIdx.x / a.splits, split = blockIdx.x - rb * a.splits;
+    const int piece = lane % S::kPieces, sub = lane / S::kPieces;
+    int64_t named[S::kX];                                // asked for beside the offsets, not after them
+#pragma unroll
+    for (int i = 0; i < S::kX; ++i) named[i] = a.row_token[(int64_t)rb * kRows + i * S::kPass + sub];
     const int e = adapter_of(a.offsets, a.E, rb * kRows, lane);
     if (e < 0 || e >= a.E) return;                       // the whole block
     // Rows of padding are loaded from row 0 and ranks past r from rank 0: what they give is not kept, and loads that
     // nothing branches around let the compiler wait for the oldest alone.
-    const int piece = lane % S::kPieces, sub = lane / S::kPieces;
     const uint16_t *x[S::kX], *w[S::kW];
 #pragma unroll
     for (int i = 0; i < S::kX; ++i) {
-        const int token = token_of(a.row_token, (int64_t)rb * kRows + i * S::kPass + sub, a.T);
+        const int token = token_of(named[i], a.T);
         x[i] = a.x + (token < 0 ? 0 : token) * a.ld + piece * 8;
     }
 #pragma unroll
@@ -203,7 +203,7 @@ __global__ __launch_bounds__(kBlock) void lora_shrink_kernel(const LoraShrink a)
         v4f v = red[0][row][q];
 #pragma unroll
         for (int n = 1; n < kWaves; ++n) v += red[n][row][q];
-        if (token_of(a.row_token, (int64_t)rb * kRows + row, a.T) < 0) v = v4f{0, 0, 0, 0};
+        if (token_of(a.row_token[(int64_t)rb * kRows + row], a.T) < 0) v = v4f{0, 0, 0, 0};
         *reinterpret_cast<v4f *>(out + (int64_t)row * a.r + q * 4) = v;
     }
 }
@@ -270,19 +270,27 @@ __global__ __launch_bounds__(kBlock, KT == 4 ? 1 : 2) void lora_expand_kernel(co
     const int group = blockIdx.x / a.step, tile0 = blockIdx.x - group * a.step;
     const int rb0 = group * RB;
     const int blocks = (int)(a.rows / kRows);
+    const int piece = lane % T::kPieces, sub = lane / T::kPieces;
+    // asked for beside the offsets, not after them
+    int64_t named[RB * 2][kPasses];
+#pragma unroll
+    for (int i = 0; i < RB * 2; ++i)
+#pragma unroll
+        for (int p = 0; p < kPasses; ++p) {
+            const int64_t row = (int64_t)rb0 * kRows + i * 16 + p * T::kPass + sub;
+            named[i][p] = a.row_token[row < a.rows ? row : 0];
+        }
     int e[RB];
 #pragma unroll
     for (int i = 0; i < RB; ++i) {
-        e[i] = rb0 + i < blocks ? adapter_of(a.offsets, a.E, (rb0 + i) * kRows, lane) : -1;
-        if (e[i] >= a.E) e[i] = -1;
+        e[i] = adapter_of(a.offsets, a.E, (rb0 + i) * kRows, lane);
+        if (e[i] >= a.E || rb0 + i >= blocks) e[i] = -1;
     }
-    const int piece = lane % T::kPieces, sub = lane / T::kPieces;
     int token[RB * 2][kPasses];
 #pragma unroll
     for (int i = 0; i < RB * 2; ++i)
 #pragma unroll
-        for (int p = 0; p < kPasses; ++p)
-            token[i][p] = e[i >> 1] < 0 ? -1 : token_of(a.row_token, (int64_t)rb0 * kRows + i * 16 + p * T::kPass + sub, a.T);
+        for (int p = 0; p < kPasses; ++p) token[i][p] = e[i >> 1] < 0 ? -1 : token_of(named[i][p], a.T);
 
     struct Ahead {
         v4u y[RB * 2][kPasses];
@@ -497,16 +505,19 @@ __global__ __launch_bounds__(kBlock) void lora_prepare_kernel(const LoraPrepare 
         for (int64_t i = (int64_t)blockIdx.x * kWaves + (threadIdx.x >> 6); i < all; i += (int64_t)gridDim.x * kWaves) {
             const int64_t rb = i / tiles;
             const int rank = (int)(i - rb * tiles) * 16 + m;
-            const int e = adapter_of(a.offsets, a.E, (int)rb * kRows, lane);
-            const bool in = e >= 0 && e < a.E && rank < a.r;
-            const float scale = in && a.scales ? a.scales[e] : 1.0f;
             float p[8];
+            int64_t named[8];
 #pragma unroll
             for (int q = 0; q < 8; ++q) {
                 const int64_t row = rb * kRows + kg * 8 + q;
-                const float v = a.hidden[row * a.r + (rank < a.r ? rank : 0)];
-                p[q] = in && token_of(a.row_token, row, a.T) >= 0 ? v * scale : 0.0f;
+                p[q] = a.hidden[row * a.r + (rank < a.r ? rank : 0)];
+                named[q] = a.row_token[row];
             }
+            const int e = adapter_of(a.offsets, a.E, (int)rb * kRows, lane);
+            const bool in = e >= 0 && e < a.E && rank < a.r;
+            const float scale = in && a.scales ? a.scales[e] : 1.0f;
+#pragma unroll
+            for (int q = 0; q < 8; ++q) p[q] = in && token_of(named[q], a.T) >= 0 ? p[q] * scale : 0.0f;
             pack_rows(p, a.packed + i * kOuterParts * 64 + lane);
         }
         return;
