@@ -145,12 +145,13 @@ mxfp8_status mxfp8_lora_add(void *y, mxfp8_dtype y_dtype, int64_t ld_y, const vo
     s.x = static_cast<const uint16_t *>(x), s.ld = ld_x, s.T = T, s.w = static_cast<const uint16_t *>(a);
     s.offsets = offsets, s.row_token = row_token, s.rows = rows, s.part = static_cast<float *>(workspace);
     s.E = (int)E, s.r = (int)r, s.K = (int)K, s.splits = cut.splits, s.slice = cut.slice;
-    if (T) st = finish(launch_lora_shrink(s, stream));
-    if (st != MXFP8_OK) return st;
     LoraExpand p{};
     p.y = y, p.ld = ld_y, p.T = T, p.w = static_cast<const uint16_t *>(b), p.scales = scales, p.offsets = offsets;
     p.row_token = row_token, p.rows = rows, p.part = s.part, p.hidden = hidden;
     p.E = T ? (int)E : 0, p.r = (int)r, p.N = T ? (int)N : 0, p.splits = cut.splits;
+    if (T && lora_both(rows, T, r, K, device_cu_count())) return finish(launch_lora_both(s, p, e == 2, stream));
+    if (T) st = finish(launch_lora_shrink(s, stream));
+    if (st != MXFP8_OK) return st;
     return finish(launch_lora_expand(p, e == 2, stream));
 }
 
@@ -202,13 +203,17 @@ mxfp8_status mxfp8_lora_backward(void *d_x, int64_t ld_dx, const void *d_y, int6
         s.x = static_cast<const uint16_t *>(d_y), s.ld = ld_dy, s.T = T, s.w = t.job[1].to, s.offsets = offsets;
         s.row_token = row_token, s.rows = rows, s.part = reinterpret_cast<float *>(base + w.part);
         s.E = (int)E, s.r = (int)r, s.K = (int)N, s.splits = w.cut.splits, s.slice = w.cut.slice;
-        st = finish(launch_lora_shrink(s, stream));
-        if (st != MXFP8_OK) return st;
         LoraExpand p{};
         p.y = d_x, p.ld = ld_dx, p.T = T, p.w = t.job[0].to, p.scales = scales, p.offsets = offsets;
         p.row_token = row_token, p.rows = rows, p.part = s.part, p.packed = s_rows;
         p.E = (int)E, p.r = (int)r, p.N = d_x ? (int)K : 0, p.splits = w.cut.splits;
-        st = finish(launch_lora_expand(p, true, stream));
+        if (lora_both(rows, T, r, N, device_cu_count())) {
+            st = finish(launch_lora_both(s, p, true, stream));
+        } else {
+            st = finish(launch_lora_shrink(s, stream));
+            if (st != MXFP8_OK) return st;
+            st = finish(launch_lora_expand(p, true, stream));
+        }
         if (st != MXFP8_OK) return st;
     }
     LoraOuter o{};

@@ -83,30 +83,31 @@ __device__ __forceinline__ int token_of(int64_t t, int64_t T) { return t >= 0 &&
 // operands are loaded in runs of 256 or 128 bytes of a row, kept in registers
 // until the chunk before is used, and turned in the wave's part of LDS: row r's
 // 16-byte piece c lies at c ^ r, which spreads 16 rows over the banks.
-template <int RT>
+template <int RT, int WAVES>
 struct ShrinkShape {
-    static constexpr int kChunk = RT <= 2 ? 128 : 64;            // columns of a wave's chunk
+    static constexpr int kChunk = RT == 1 || (RT == 2 && WAVES == 4) ? 128 : 64;         // columns of a wave's chunk
     static constexpr int kPieces = kChunk / 8;                   // 16-byte pieces of a row of it
     static constexpr int kPass = 64 / kPieces;                   // rows that a wave loads at once
     static constexpr int kX = kRows / kPass, kW = RT * 16 / kPass;
     static constexpr int kWaveBytes = (kRows + RT * 16) * kChunk * 2;
-    static constexpr int kRedBytes = kWaves * kRows * RT * 64;
-    static constexpr int kBytes = kWaves * kWaveBytes > kRedBytes ? kWaves * kWaveBytes : kRedBytes;
+    static constexpr int kRedBytes = WAVES * kRows * RT * 64;
+    static constexpr int kBytes = WAVES * kWaveBytes > kRedBytes ? WAVES * kWaveBytes : kRedBytes;
 };
 
-template <int RT>
-__global__ __launch_bounds__(kBlock) void lora_shrink_kernel(const LoraShrink a) {
-    using S = ShrinkShape<RT>;
-    __shared__ v4u room[S::kBytes / 16];
+// Columns [k_first, k1) of block rb's rows against its adapter's weights: the
+// waves' sums in `room`, [WAVES][32][RT * 4], four ranks each.  Whether the rows
+// have an adapter is the same for the whole block.
+template <int RT, int WAVES>
+__device__ __forceinline__ bool shrink_rows(const LoraShrink &a, int rb, int k_first, int k1, v4u *room) {
+    using S = ShrinkShape<RT, WAVES>;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int m = lane & 15, kg = lane >> 4;
-    const int rb = blockIdx.x / a.splits, split = blockIdx.x - rb * a.splits;
     const int piece = lane % S::kPieces, sub = lane / S::kPieces;
     int64_t named[S::kX];                                // asked for beside the offsets, not after them
 #pragma unroll
     for (int i = 0; i < S::kX; ++i) named[i] = a.row_token[(int64_t)rb * kRows + i * S::kPass + sub];
     const int e = adapter_of(a.offsets, a.E, rb * kRows, lane);
-    if (e < 0 || e >= a.E) return;                       // the whole block
+    if (e < 0 || e >= a.E) return false;
     // Rows of padding are loaded from row 0 and ranks past r from rank 0: what they give is not kept, and loads that
     // nothing branches around let the compiler wait for the oldest alone.
     const uint16_t *x[S::kX], *w[S::kW];
@@ -126,7 +127,6 @@ __global__ __launch_bounds__(kBlock) void lora_shrink_kernel(const LoraShrink a)
 #pragma unroll
         for (int j = 0; j < RT; ++j) acc[t][j] = v4f{0, 0, 0, 0};
 
-    const int k1 = min(a.K, (split + 1) * a.slice);
     v4u xs[S::kX], ws[S::kW];
     auto ask = [&](int k0) {
 #pragma unroll
@@ -172,8 +172,8 @@ __global__ __launch_bounds__(kBlock) void lora_shrink_kernel(const LoraShrink a)
         }
         wave_sync();
     };
-    constexpr int kStep = kWaves * S::kChunk;
-    int k0 = split * a.slice + wave * S::kChunk;
+    constexpr int kStep = WAVES * S::kChunk;
+    int k0 = k_first + wave * S::kChunk;
     if (k0 + S::kChunk <= k1) {
         ask(k0);
         for (; k0 + S::kChunk <= k1; k0 += kStep) {
@@ -196,6 +196,15 @@ __global__ __launch_bounds__(kBlock) void lora_shrink_kernel(const LoraShrink a)
 #pragma unroll
         for (int j = 0; j < RT; ++j) red[wave][t * 16 + m][j * 4 + kg] = acc[t][j];
     __syncthreads();
+    return true;
+}
+
+template <int RT>
+__global__ __launch_bounds__(kBlock) void lora_shrink_kernel(const LoraShrink a) {
+    __shared__ v4u room[ShrinkShape<RT, kWaves>::kBytes / 16];
+    const int rb = blockIdx.x / a.splits, split = blockIdx.x - rb * a.splits;
+    if (!shrink_rows<RT, kWaves>(a, rb, split * a.slice, min(a.K, (split + 1) * a.slice), room)) return;
+    auto red = reinterpret_cast<v4f (*)[kRows][RT * 4]>(room);
     float *out = a.part + ((int64_t)split * a.rows + (int64_t)rb * kRows) * a.r;
     for (int i = threadIdx.x; i < kRows * RT * 4; i += kBlock) {
         const int row = i / (RT * 4), q = i - row * (RT * 4);
@@ -252,22 +261,30 @@ struct Tile {
 // B's rows are r long, so 64 of them are one run of memory.  Above rank 32 they
 // are loaded as such and turned in LDS; loaded straight into fragments they
 // would touch a cache line for every 16 bytes (twice the time of y itself).
-template <class Y, int KT, int RB, bool LOOP>
-__global__ __launch_bounds__(kBlock, KT == 4 ? 1 : 2) void lora_expand_kernel(const LoraExpand a) {
+template <class Y, int KT, int RB, int WAVES>
+struct ExpandShape {
+    static constexpr int kParts = sizeof(Y) == 4 ? 3 : 2;
+    static constexpr bool kTurnB = KT > 1;
+    static constexpr int kB = 4 * KT;                            // 16-byte pieces of a row of B, and of a lane's B
+    typedef v4u Frag[RB * 2][KT][kParts][64];                    // P of each 16 rows as the matrix unit takes it, in parts
+    typedef float Turn[WAVES][16][68];                           // 4 more than a row: 16 rows on all banks
+    static constexpr int kBs = kTurnB ? WAVES * 64 * kB : 1;     // pieces of B
+};
+// sum(row, j, v): P of a row of the block, ranks j to j + 7
+template <class Y, int KT, int RB, bool LOOP, int WAVES, class Sum>
+__device__ __forceinline__ void expand_rows(const LoraExpand &a, int group, int tile0,
+                                            typename ExpandShape<Y, KT, RB, WAVES>::Frag &frag,
+                                            typename ExpandShape<Y, KT, RB, WAVES>::Turn &turn, v4u *bs, Sum sum) {
     using T = Tile<Y>;
-    constexpr int kParts = sizeof(Y) == 4 ? 3 : 2, kPasses = T::kPasses;
-    __shared__ v4u frag[RB * 2][KT][kParts][64];         // P of each 16 rows as the matrix unit takes it, in parts
-    __shared__ float turn[kWaves][16][68];               // 4 more than a row: 16 rows on all banks
-    constexpr bool kTurnB = KT > 1;
-    constexpr int kB = 4 * KT;                           // 16-byte pieces of a row of B, and of a lane's B
-    __shared__ v4u bs[kTurnB ? kWaves * 64 * kB : 1];
+    using S = ExpandShape<Y, KT, RB, WAVES>;
+    constexpr int kParts = S::kParts, kPasses = T::kPasses, kB = S::kB;
+    constexpr bool kTurnB = S::kTurnB;
     // scaled P of the block's rows, first 64 ranks and the rest, before what `turn` and `bs` are for
     auto flat = reinterpret_cast<float (*)[68]>(&turn[0][0][0]);
     auto upper = reinterpret_cast<float (*)[68]>(&bs[0]);
-    static_assert(RB * 32 * 68 * 4 <= sizeof(turn) && (KT < 4 || RB * 32 * 68 * 4 <= sizeof(bs)), "P's rows fit");
+    static_assert(RB * 32 * 68 * 4 <= sizeof(turn) && (KT < 4 || RB * 32 * 68 * 4 <= S::kBs * 16), "P's rows fit");
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int m = lane & 15, kg = lane >> 4;
-    const int group = blockIdx.x / a.step, tile0 = blockIdx.x - group * a.step;
     const int rb0 = group * RB;
     const int blocks = (int)(a.rows / kRows);
     const int piece = lane % T::kPieces, sub = lane / T::kPieces;
@@ -413,7 +430,7 @@ __global__ __launch_bounds__(kBlock, KT == 4 ? 1 : 2) void lora_expand_kernel(co
             }
         }
     };
-    const int first = (tile0 * kWaves + wave) * 64, step = a.step * kWaves * 64;
+    const int first = (tile0 * WAVES + wave) * 64, step = a.step * WAVES * 64;
     int start = 0;                                       // the first group that has an adapter
 #pragma unroll
     for (int i = RB - 1; i >= 0; --i) start = e[i] >= 0 ? i : start;
@@ -421,21 +438,14 @@ __global__ __launch_bounds__(kBlock, KT == 4 ? 1 : 2) void lora_expand_kernel(co
     Ahead ahead[1 + LOOP];
     if (lead >= 0 && first < a.N) ask(ahead[0], lead, first);
 
-    for (int i = threadIdx.x; i < RB * 2 * KT * 64; i += kBlock) {
+    for (int i = threadIdx.x; i < RB * 2 * KT * 64; i += WAVES * 64) {
         const int l = i & 63, kt = (i >> 6) % KT, mt = (i >> 6) / KT;
         const int ee = RB == 1 || mt < 2 ? e[0] : e[RB - 1];
         const int64_t row = (int64_t)rb0 * kRows + mt * 16 + (l & 15);
         const int j = kt * 32 + (l >> 4) * 8;
         float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
         const bool in = j < a.r && row < a.rows;
-        if (in && ee >= 0) {
-            const float *p = a.part + row * a.r + j;
-            for (int s = 0; s < a.splits; ++s, p += a.rows * a.r) {
-                const v4f lo = *reinterpret_cast<const v4f *>(p), hi = *reinterpret_cast<const v4f *>(p + 4);
-#pragma unroll
-                for (int q = 0; q < 4; ++q) v[q] += lo[q], v[4 + q] += hi[q];
-            }
-        }
+        if (in && ee >= 0) sum(row, j, v);
         if (a.hidden && tile0 == 0 && in) {
             float *h = a.hidden + row * a.r + j;
             *reinterpret_cast<v4f *>(h) = v4f{v[0], v[1], v[2], v[3]};
@@ -467,7 +477,7 @@ __global__ __launch_bounds__(kBlock, KT == 4 ? 1 : 2) void lora_expand_kernel(co
     __syncthreads();
     if (a.packed && tile0 == 0) {
         const int tiles = (a.r + 15) / 16;
-        for (int i = wave; i < RB * tiles; i += kWaves) {
+        for (int i = wave; i < RB * tiles; i += WAVES) {
             const int rb = rb0 + i / tiles, jt = i % tiles;
             if (rb >= blocks) break;
             float p[8];
@@ -490,6 +500,50 @@ __global__ __launch_bounds__(kBlock, KT == 4 ? 1 : 2) void lora_expand_kernel(co
         if (whole) columns(std::true_type(), ahead, adapter, first, step);
         else columns(std::false_type(), ahead, adapter, first, step);
     }
+}
+
+template <class Y, int KT, int RB, bool LOOP>
+__global__ __launch_bounds__(kBlock, KT == 4 ? 1 : 2) void lora_expand_kernel(const LoraExpand a) {
+    using S = ExpandShape<Y, KT, RB, kWaves>;
+    __shared__ typename S::Frag frag;
+    __shared__ typename S::Turn turn;
+    __shared__ v4u bs[S::kBs];
+    const int group = blockIdx.x / a.step;
+    expand_rows<Y, KT, RB, LOOP, kWaves>(a, group, blockIdx.x - group * a.step, frag, turn, bs, [&](int64_t row, int j, float (&v)[8]) {
+        const float *p = a.part + row * a.r + j;
+        for (int s = 0; s < a.splits; ++s, p += a.rows * a.r) {
+            const v4f lo = *reinterpret_cast<const v4f *>(p), hi = *reinterpret_cast<const v4f *>(p + 4);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) v[q] += lo[q], v[4 + q] += hi[q];
+        }
+    });
+}
+
+// Both in one launch: each block takes the whole product with A of its 32 rows,
+// and its share of the columns of y.  Blocks beside each other on the same rows
+// take that product each for itself.  The sums over ranks stay in LDS (no
+// partials in memory), and eight waves join them once.
+constexpr int kBothWaves = 8;
+template <class Y, int RT>
+__global__ __launch_bounds__(kBothWaves * 64) void lora_both_kernel(const LoraShrink s, const LoraExpand a) {
+    constexpr int KT = RT == 4 ? 2 : 1;
+    using S = ExpandShape<Y, KT, 1, kBothWaves>;
+    constexpr int kRoom = ShrinkShape<RT, kBothWaves>::kBytes / 16;
+    __shared__ v4u room[kRoom > S::kBs ? kRoom : S::kBs];        // the sums, then B
+    __shared__ typename S::Frag frag;
+    __shared__ typename S::Turn turn;
+    const int rb = blockIdx.x / a.step;
+    shrink_rows<RT, kBothWaves>(s, rb, 0, s.K, room);
+    auto red = reinterpret_cast<const v4f (*)[kRows][RT * 4]>(room);
+    expand_rows<Y, KT, 1, true, kBothWaves>(a, rb, blockIdx.x - rb * a.step, frag, turn, room, [&](int64_t row, int j, float (&v)[8]) {
+        if (j >= RT * 16 || token_of(a.row_token[row], a.T) < 0) return;
+        const int at = (int)(row - (int64_t)rb * kRows);
+        for (int n = 0; n < kBothWaves; ++n) {
+            const v4f lo = red[n][at][j >> 2], hi = red[n][at][(j >> 2) + 1];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) v[q] += lo[q], v[4 + q] += hi[q];
+        }
+    });
 }
 
 // ---------------------------------------------------------------- before the gradients
@@ -889,6 +943,12 @@ void start_expand(const LoraExpand &a, int cus, hipStream_t stream) {
     else if (a.r <= 64) start_expand<Y, 2>(a, cus, stream);
     else start_expand<Y, 4>(a, cus, stream);
 }
+template <class Y>
+void start_both(const LoraShrink &s, const LoraExpand &a, unsigned grid, hipStream_t stream) {
+    if (a.r <= 16) lora_both_kernel<Y, 1><<<grid, kBothWaves * 64, 0, stream>>>(s, a);
+    else if (a.r <= 32) lora_both_kernel<Y, 2><<<grid, kBothWaves * 64, 0, stream>>>(s, a);
+    else lora_both_kernel<Y, 4><<<grid, kBothWaves * 64, 0, stream>>>(s, a);
+}
 template <int RT>
 void start_outer(const LoraOuter &a, int form, unsigned grid, hipStream_t stream) {
     if (form == 0) lora_outer_kernel<RT, WideBf16><<<grid, kBlock, 0, stream>>>(a);
@@ -922,6 +982,32 @@ hipError_t launch_lora_expand(LoraExpand a, bool y_bf16, hipStream_t stream) {
     const int cus = device_cu_count();
     if (y_bf16) start_expand<uint16_t>(a, cus, stream);
     else start_expand<float>(a, cus, stream);
+    return hipGetLastError();
+}
+
+// One launch instead of two.  Where there is a block of rows for more than every
+// second CU, no block takes what another one takes too (7936 rows of rank 64,
+// 4096 to 6144: 51.3 us for 61.1; the other way round only for 4320 rows of rank
+// 64 and 12288 columns, 52.5 for 49.3), up to the padding of a batch that fills
+// the CUs once (8192 rows of 8 adapters, 263 blocks: 56.7 for 64.6; at 391 blocks
+// 95.7 for 94.8, with 12288 columns 165 for 145).  With fewer blocks, where a
+// block's rows of x and A are short enough that taking them several times costs
+// less than the second launch (one row of rank 16, 4096 to 6144: 10.4 us for 13.2
+// with the host's part, 64 rows of as many adapters 13.1 for 13.5; past the bound
+// 512 rows of 8 adapters take 15.2 for 13.0, one row of 12288 columns 15.4 for 13.1).
+bool lora_both(int64_t rows, int64_t T, int64_t r, int64_t K, int cus) {
+    const int64_t blocks = rows / kRows, most = 96 * 1024;
+    if (r > 64 || blocks > cus + cus / 16) return false;
+    const int64_t used = ceil_div(T, blocks);
+    return blocks > cus / 2 || (K <= most && K * ((used < kRows ? used : kRows) + r) <= most);
+}
+
+hipError_t launch_lora_both(const LoraShrink &s, LoraExpand a, bool y_bf16, hipStream_t stream) {
+    const int64_t blocks = a.rows / kRows, tiles = a.N ? ceil_div(a.N, kBothWaves * 64) : 1;
+    const int64_t step = device_cu_count() / blocks;
+    a.step = (int)(step < 1 ? 1 : step < tiles ? step : tiles);
+    if (y_bf16) start_both<uint16_t>(s, a, (unsigned)(blocks * a.step), stream);
+    else start_both<float>(s, a, (unsigned)(blocks * a.step), stream);
     return hipGetLastError();
 }
 

@@ -294,6 +294,9 @@ struct LoraExpand {
     int step;                   // set by the launcher: blocks beside each other on the same rows
 };
 hipError_t launch_lora_expand(LoraExpand a, bool y_bf16, hipStream_t stream);
+// both in one launch, without partials, where lora_both says so
+bool lora_both(int64_t rows, int64_t T, int64_t r, int64_t K, int cus);
+hipError_t launch_lora_both(const LoraShrink &s, LoraExpand a, bool y_bf16, hipStream_t stream);
 struct LoraPrepare {
     struct Job {
         const uint16_t *from;   // [E][P][Q]
