@@ -556,7 +556,10 @@ void start_rows(const DraftArgs &a, int cus, hipStream_t stream) {
 }
 template <class E>
 void start(const DraftArgs &a, int cus, hipStream_t stream) {
-    start_rows<E, false>(a, cus, stream);
+    // Past the caches where the logits are more than 3/8 of the last level, although the draws read some rows again:
+    // 134 MB of bf16 logits 49.8 -> 47.0 us in all, 81 MB of fp32 logits 31.7 -> 32.7.
+    if (a.rows * a.V * (int64_t)sizeof(E) > kLastLevelBytes / 8 * 3) start_rows<E, true>(a, cus, stream);
+    else start_rows<E, false>(a, cus, stream);
     draft_draw_kernel<E><<<(unsigned)(a.B * a.cuts), kBlock, 0, stream>>>(a);
     draft_finish_kernel<E><<<(unsigned)a.B, kWide, 0, stream>>>(a);
 }
