@@ -97,7 +97,7 @@ size_t mxfp8_lora_add_workspace_bytes(int64_t rows, int64_t E, int64_t r, int64_
 /*
  * mxfp8_lora_add -- y += the adapters' products, in place.
  *   y : [T][N] FP32 or BF16, rows ld_y >= N elements apart; rows without an
- *       adapter are neither read nor written
+ *       adapter are left as they are
  *   hidden : or NULL; kept for mxfp8_lora_backward
  *   workspace : mxfp8_lora_add_workspace_bytes(..) bytes, 16-byte aligned
  */

@@ -3,9 +3,9 @@
 //
 // A group's rows start at a multiple of 32, so every block of 32 sorted rows
 // has one adapter and its products run on the matrix unit.  The rank is small:
-// every product reads or writes one wide matrix once and is bound by that, so
-// operands go from global memory straight into matrix fragments (the weights'
-// and hidden rows' fragments come from the caches) and LDS only joins waves.
+// every product reads or writes one wide matrix once, and what bounds it is how
+// that matrix moves.  Operands are loaded in runs of a row and turned in LDS or
+// in registers; the weights and P come from the caches.
 //
 //   shrink   P = X A^T          partial sums over slices of the wide axis
 //   expand   Y += (s P) B^T     sums the partials, keeps P
@@ -75,7 +75,9 @@ __device__ __forceinline__ int token_of(int64_t t, int64_t T) { return t >= 0 &&
 // ---------------------------------------------------------------- shrink
 
 // One block: 32 sorted rows, a slice of the wide axis, all ranks.  Its waves
-// take chunks of it in turn, each on its own.  RT: tiles of 16 ranks.
+// take chunks of it in turn, each on its own.  RT: tiles of 16 ranks.  Bound by
+// loads in flight: 8192 rows of 4096, rank 64, by itself 28 us (67 MB, 2.4 TB/s;
+// 11 us of it the launch, the first loads and the join).
 //
 // The matrix unit wants 16 rows from 16 neighbouring lanes, and a load that is
 // laid out so touches 16 cache lines with every 256 bytes it brings (8192 rows
@@ -256,7 +258,9 @@ struct Tile {
 // 16 rows, 16 cache lines for 256 bytes).  The next columns' y and B are asked
 // for before the current ones are used.  Joining P once for many columns
 // matters: 8192 rows of rank 64 to 6144 take 60 us with P joined for every 256.
-// KT: steps of 32 ranks.  LOOP: several columns.
+// KT: steps of 32 ranks.  LOOP: several columns.  By itself rank 64 to 8192 x 6144
+// takes 51 us, rank 32 to 8192 x 4096 31 us; y alone, read and written in place
+// (201 MB), takes 37.4 at its best.
 //
 // B's rows are r long, so 64 of them are one run of memory.  Above rank 32 they
 // are loaded as such and turned in LDS; loaded straight into fragments they
@@ -522,7 +526,9 @@ __global__ __launch_bounds__(kBlock, KT == 4 ? 1 : 2) void lora_expand_kernel(co
 // Both in one launch: each block takes the whole product with A of its 32 rows,
 // and its share of the columns of y.  Blocks beside each other on the same rows
 // take that product each for itself.  The sums over ranks stay in LDS (no
-// partials in memory), and eight waves join them once.
+// partials in memory), and eight waves join them once.  8192 rows of rank 64, 4096
+// to 6144: 55 us on one input, 73 with inputs that change (270 MB, 3.7 TB/s): a
+// compute unit's waves first all read x and then all update y.
 constexpr int kBothWaves = 8;
 template <class Y, int RT>
 __global__ __launch_bounds__(kBothWaves * 64) void lora_both_kernel(const LoraShrink s, const LoraExpand a) {
@@ -550,6 +556,7 @@ __global__ __launch_bounds__(kBothWaves * 64) void lora_both_kernel(const LoraSh
 
 // The weights transposed, [E][P][Q] -> [E][Q][P] in 64 x 64 tiles (P and Q
 // multiples of 8), and the hidden rows, scaled, as the outer products take them.
+// A small launch: 4 to 5 us.
 __global__ __launch_bounds__(kBlock) void lora_prepare_kernel(const LoraPrepare a) {
     __shared__ uint16_t t[64][72];
     if (blockIdx.y == 2) {
@@ -815,7 +822,9 @@ __device__ __forceinline__ void outer_rows(const LoraOuter &a, const LoraWide &w
 // One block: an item's rows, 128 columns of a wide matrix, RT tiles of 16
 // ranks.  A lane loads 8 columns of 8 rows and turns them into eight fragments
 // with one permutation for every two values, so nothing is staged.  Its waves
-// take blocks of 32 rows in turn.
+// take blocks of 32 rows in turn.  8192 rows of rank 32, x [4096] in 8 bits and d_y
+// [6144]: 35 to 40 us (134 MB, 3.4 TB/s), half of it vector arithmetic on the
+// values' forms; 4001 rows of rank 16, 2048 and 1536 in bf16: 12.8 us.
 template <int RT, class Wide, bool SECOND>
 __device__ __forceinline__ void outer_block(const LoraOuter &a, const Item &it, int slab, int j0, int lane, int wave,
                                             v4u (&red)[2][RT * 8][64]) {
@@ -885,7 +894,7 @@ __global__ __launch_bounds__(kBlock, RT <= 2 ? 2 : 1) void lora_outer_kernel(con
 }
 
 // The sums of adapters with several items, slots in order; block row y is the
-// y-th such adapter
+// y-th such adapter.  4 to 5 us.
 __global__ __launch_bounds__(kBlock) void lora_join_kernel(const LoraOuter a) {
     const int lane = threadIdx.x & 63;
     Scan before{0, 0, 0, 0};
@@ -925,7 +934,7 @@ template <class Y, int KT>
 void start_expand(LoraExpand a, int cus, hipStream_t stream) {
     // Blocks of 64 rows (32 where y is fp32) that go through several columns each, as many as are resident at once (by
     // their registers two a compute unit, one for ranks above 64), where there are that many columns; else of 32 rows
-    // and 256 columns.
+    // and 256 columns (8192 rows of rank 64 to 6144 so 60 us for 51).
     constexpr int kWide = sizeof(Y) == 4 ? 1 : 2, kResident = KT == 4 ? 1 : 2;
     const int64_t blocks = a.rows / kRows, groups = ceil_div(blocks, kWide), tiles = a.N ? ceil_div(a.N, 256) : 1;
     if (groups * tiles >= 2 * kResident * cus) {
@@ -960,7 +969,8 @@ void start_outer(const LoraOuter &a, int form, unsigned grid, hipStream_t stream
 
 LoraCut lora_cut(int64_t rows, int64_t K, int cus) {
     // blocks of 32 rows; the wide axis is cut where they alone do not fill the compute units twice, into slices that
-    // give every wave of a block a chunk
+    // give every wave of a block a chunk (one row of 12288, rank 16: 15.4 us whole, 10.6 cut, the launch of both products
+    // in it)
     const int64_t blocks = rows / kRows, most = ceil_div(K, kWaves * 128);
     int64_t splits = blocks ? ceil_div(2 * cus, blocks) : 1;
     splits = splits < most ? splits : most;
