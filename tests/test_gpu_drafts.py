@@ -327,3 +327,13 @@ def test_streams_and_graphs(mx):
         torch.cuda.synchronize()
         assert torch.equal(out.accepted, want[n].accepted) and torch.equal(out.tokens, want[n].tokens)
         assert torch.equal(out.logprobs, want[n].logprobs)
+
+
+def test_logits_past_the_caches(mx):
+    """More than 96 MB of fp32 logits with rows at any 4 bytes, and of bf16 ones without a draft at any 2"""
+    case = _case([5] * 36, 70001, torch.float32, 9)
+    assert (case[0].numel() + case[5].numel()) * 4 > 96 << 20
+    _check(mx, *case)
+    case = _case([0, 5, 3, 7] * 30, 120001, torch.bfloat16, 10, draft=False)
+    assert case[0].numel() * 2 > 96 << 20
+    _check(mx, *case)

@@ -211,3 +211,32 @@ def test_more_than_2_31_elements(mx):
         assert torch.equal(part.saved_q, r.saved_q[rows]) and torch.equal(part.saved_s, r.saved_s[rows])
         want = mx.swiglu_backward(d[rows], part.saved_q, part.saved_s)
         assert torch.equal(want[0], d_gu[rows]) and torch.equal(want[1], h[rows])
+
+
+@pytest.mark.parametrize("layout", ["bf16", "canonical", "packed"])
+def test_passes_larger_than_the_last_level_cache(mx, layout):
+    """In every form, with and without a checkpoint, against calls of a few rows (which keep to the caches)"""
+    T, inner = 1721, 32 * 1223                           # 67 million elements of h: past 256 MB in every form
+    gu = _gu(T, inner, seed=4)
+    r, bare = mx.swiglu(gu, layout=layout), mx.swiglu(gu, layout=layout, save=False)
+    d_h = gu[:, inner:]
+    d_gu, h = mx.swiglu_backward(d_h, r.saved_q, r.saved_s)
+    alone, none = mx.swiglu_backward(d_h, r.saved_q, r.saved_s, recompute=False)
+    assert none is None and torch.equal(alone, d_gu)
+    parts = [slice(i, min(i + 256, T)) for i in range(0, T, 256)]
+    small = [mx.swiglu(gu[p], layout="bf16" if layout == "bf16" else "canonical") for p in parts]
+    assert torch.equal(r.saved_q, torch.cat([s.saved_q for s in small])) and torch.equal(r.saved_s, torch.cat([s.saved_s for s in small]))
+    if layout == "bf16":
+        want = torch.cat([s.h for s in small])
+        assert torch.equal(r.h, want) and torch.equal(bare.h, want)
+    else:
+        q, s = (torch.cat([part.h[i] for part in small]) for i in (0, 1))
+        if layout == "packed":
+            w = mx.repack(q.view(1, T, inner), s.view(1, T, inner // 32))
+            q, s = w.q, w.s
+        for got in (r.h, bare.h):
+            a, b = (got.q, got.s) if layout == "packed" else got
+            assert torch.equal(a.view(-1), q.view(-1)) and torch.equal(b.view(-1), s.view(-1))
+    for p, part in zip(parts, small):
+        want = mx.swiglu_backward(d_h[p], part.saved_q, part.saved_s)
+        assert torch.equal(d_gu[p], want[0]) and torch.equal(h[p], want[1])
