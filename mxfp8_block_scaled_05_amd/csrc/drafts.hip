@@ -113,7 +113,7 @@ __device__ __forceinline__ const E *row_of(const DraftArgs &a, int64_t i) {
 }
 
 // One pass, bound by HBM where there are many: 512 rows of 131072 bf16 (134 MB)
-// 24 us, 5.5 TB/s with the vector ALU at 71%; 198 rows of 100003 fp32 15 us, 5.3.
+// 22.7 us, 5.9 TB/s with the vector ALU at 66%; 198 rows of 100003 fp32 15 us, 5.3.
 template <class E, int BLOCK, bool ONCE>
 __global__ __launch_bounds__(BLOCK) void draft_rows_kernel(const DraftArgs a) {
     constexpr int kV = Elem<E>::kVec, kWaves = BLOCK / 64, kStep = BLOCK * kV;
@@ -563,7 +563,7 @@ void start_rows(const DraftArgs &a, int cus, hipStream_t stream) {
 template <class E>
 void start(const DraftArgs &a, int cus, hipStream_t stream) {
     // Past the caches where the logits are more than 3/8 of the last level, although the draws read some rows again:
-    // 134 MB of bf16 logits 49.8 -> 47.0 us in all, 81 MB of fp32 logits 31.7 -> 32.7.
+    // 134 MB of bf16 logits 48.0 -> 45.3 us in all, 81 MB of fp32 logits 32.3 -> 32.6.
     if (a.rows * a.V * (int64_t)sizeof(E) > kLastLevelBytes / 8 * 3) start_rows<E, true>(a, cus, stream);
     else start_rows<E, false>(a, cus, stream);
     draft_draw_kernel<E><<<(unsigned)(a.B * a.cuts), kBlock, 0, stream>>>(a);

@@ -2,8 +2,8 @@
 // the backward pass, and its gradient from that checkpoint.
 //
 // Both directions stream, and HBM bounds them: 8192 x 12288 (714 MB with the
-// checkpoint and codes of h) in 116 us, the gradient of 4095 x 12288 (507 MB) in
-// 82 us, 6.2 TB/s both.  A lane owns 8 columns of gate and the same 8 of up,
+// checkpoint and codes of h) in 116 us (its vector arithmetic takes as long), the
+// gradient of 4095 x 12288 (507 MB) in 82 us, 6.2 TB/s both.  A lane owns 8 columns of gate and the same 8 of up,
 // so that a wave's accesses are whole runs of 1 KB (512 B of codes), and four
 // lanes share a block's scale; with 16 columns a lane, two accesses of every
 // second 16 bytes, the same take 142 and 107.  Everything that the values lead
