@@ -997,8 +997,9 @@ hipError_t launch_lora_expand(LoraExpand a, bool y_bf16, hipStream_t stream) {
 
 // One launch instead of two.  Where there is a block of rows for more than every
 // second CU, no block takes what another one takes too (7936 rows of rank 64,
-// 4096 to 6144: 51.3 us for 61.1; the other way round only for 4320 rows of rank
-// 64 and 12288 columns, 52.5 for 49.3), up to the padding of a batch that fills
+// 4096 to 6144: 51.3 us for 61.1; 4320 rows, 135 blocks, at worst 52.5 for 49.3 with
+// 12288 columns of x, but 120 for 77 with 32768, which few blocks read too slowly:
+// there from two of three CUs on, 182 blocks 135 for 146), up to the padding of a batch that fills
 // the CUs once (8192 rows of 8 adapters, 263 blocks: 56.7 for 64.6; at 391 blocks
 // 95.7 for 94.8, with 12288 columns 165 for 145).  With fewer blocks, where a
 // block's rows of x and A are short enough that taking them several times costs
@@ -1009,7 +1010,8 @@ bool lora_both(int64_t rows, int64_t T, int64_t r, int64_t K, int cus) {
     const int64_t blocks = rows / kRows, most = 96 * 1024;
     if (r > 64 || blocks > cus + cus / 16) return false;
     const int64_t used = ceil_div(T, blocks);
-    return blocks > cus / 2 || (K <= most && K * ((used < kRows ? used : kRows) + r) <= most);
+    if (blocks > (K <= 16384 ? cus / 2 : cus * 2 / 3)) return true;
+    return K <= most && K * ((used < kRows ? used : kRows) + r) <= most;
 }
 
 hipError_t launch_lora_both(const LoraShrink &s, LoraExpand a, bool y_bf16, hipStream_t stream) {

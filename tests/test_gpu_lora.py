@@ -400,7 +400,8 @@ def test_malformed_tables_stay_inside(mx):
 # Sizes on both sides of the rule that takes both products in one launch (rank up to 64): below it by the length of a
 # block's rows, by blocks for every second CU, and above it by more blocks than there are CUs.
 RULE = [(1, 1, 16, 6128, 200), (1, 1, 16, 6144, 200), (512, 8, 16, 4096, 1032), (90, 3, 64, 2056, 328), (90, 3, 32, 4104, 72),
-        (4200, 3, 64, 264, 584), (8600, 9, 40, 72, 136), (8900, 5, 16, 136, 264), (9100, 2, 64, 200, 456), (9100, 2, 32, 520, 64)]
+        (4200, 3, 64, 264, 584), (8600, 9, 40, 72, 136), (8900, 5, 16, 136, 264), (9100, 2, 64, 200, 456), (9100, 2, 32, 520, 64),
+        (4200, 3, 16, 16392, 72)]
 
 
 @pytest.mark.parametrize("T,E,r,K,N", RULE)
