@@ -88,7 +88,8 @@ mxfp8_status mxfp8_swiglu_backward(const void *d_h_bf16, int64_t ld, int64_t T, 
  * N) < 2^40; all pointers 16-byte aligned but offsets and scales (4) and row_token (8).  T = 0: every row is padding.
  * The adapters' sums are held in fp32; A x and S enter the next product as sums
  * of BF16 numbers that keep all 24 bits where the result is FP32, 16 where it
- * is BF16.
+ * is BF16.  An infinity among the operands, and a product that leaves FP32's
+ * range, give the infinity or NaN that the formula gives.
  */
 
 /* Workspace bytes of mxfp8_lora_add (0 for invalid sizes). */

@@ -19,6 +19,11 @@
 // (y, the weights' gradients), two, which lose 2^-16 of the value, where it is
 // rounded to bf16 (2^-8).  The products of the parts cost matrix time that is
 // idle anyway: these kernels wait for memory.
+//
+// The parts of a finite P may be 0 or differ in sign, so against an infinity, or
+// where a product leaves fp32, they make a NaN of what is an infinity.  The
+// first part alone, which has P's sign and is 0 only with it, decides there: a
+// NaN among the sums has its tile's products taken again with that part.
 #include <type_traits>
 
 #include "mx_launch.hpp"
@@ -51,6 +56,21 @@ __device__ __forceinline__ void split_pair(float v0, float v1, uint32_t (&out)[N
         v0 = rest_of(v0, __uint_as_float(out[n] << 16));
         v1 = rest_of(v1, __uint_as_float(out[n] & 0xFFFF0000u));
     }
+}
+
+// Whether one of a lane's sums is a NaN; four sums with those of `first` in
+// such places
+template <int N>
+__device__ __forceinline__ bool has_nan(const v4f (&d)[N]) {
+    bool nan = false;
+#pragma unroll
+    for (int n = 0; n < N; ++n) nan = nan || __builtin_isunordered(d[n].x, d[n].y) || __builtin_isunordered(d[n].z, d[n].w);
+    return nan;
+}
+__device__ __forceinline__ v4f instead_of_nan(v4f d, v4f first) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) d[i] = d[i] == d[i] ? d[i] : first[i];
+    return d;
 }
 
 // The compiler moves a load to where its value is first used, a round later,
@@ -401,6 +421,21 @@ __device__ __forceinline__ void expand_rows(const LoraExpand &a, int group, int 
             }
 #pragma unroll
             for (int q = 0; q < 4; ++q) *reinterpret_cast<v4f *>(&turn[wave][m][q * 16 + kg * 4]) = d[q];
+            if (__builtin_expect(__ballot(has_nan(d)) != 0, 0)) {
+#pragma unroll 1
+                for (int q = 0; q < 4; ++q) {
+                    v4f first = {0, 0, 0, 0};
+#pragma unroll 1
+                    for (int kt = 0; kt < KT; ++kt) {
+                        v4u b;
+                        if constexpr (kTurnB) b = mine[slot(q * 16 + m, kt * 4 + kg)];
+                        else b = q == 0 ? n.b[0] : q == 1 ? n.b[1] : q == 2 ? n.b[2] : n.b[3];
+                        first = mfma(b, frag[i][kt][0][lane], first);
+                    }
+                    auto sums = reinterpret_cast<v4f *>(&turn[wave][m][q * 16 + kg * 4]);          // this lane's
+                    *sums = instead_of_nan(*sums, first);
+                }
+            }
             wave_sync();
 #pragma unroll
             for (int p = 0; p < kPasses; ++p) {
@@ -819,6 +854,41 @@ __device__ __forceinline__ void outer_rows(const LoraOuter &a, const LoraWide &w
     }
 }
 
+// Where the item's sums at `out` are NaN: those of P's first parts alone.  By
+// the wave that wrote them, over all of the item's rows.
+template <int RT, class Wide, bool SECOND>
+__device__ __forceinline__ void outer_first(const LoraOuter &a, const LoraWide &w, const Item &it, int j0, int col, bool in, int lane,
+                                            float *out) {
+    const int kg = lane >> 4, tiles = (a.r + 15) / 16;
+#pragma unroll 1
+    for (int jt = j0 / 16; jt < min(j0 / 16 + RT, tiles); ++jt) {
+        v4f first[8];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) first[c] = v4f{0, 0, 0, 0};
+#pragma unroll 1
+        for (int row = it.row0; row < it.row1; row += kRows) {
+            int token[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) token[i] = token_of(a.row_token[row + kg * 8 + i], a.T);
+            Wide x;
+            x.load(w, token, col, in);
+            x.settle();
+            const v4u p = w.p[((int64_t)(row >> 5) * tiles + jt) * kOuterParts * 64 + lane];
+#pragma unroll
+            for (int c = 0; c < 8; ++c) first[c] = mfma(p, x.column(c), first[c]);
+        }
+        const int rank = jt * 16 + kg * 4;
+        if (!in || rank >= a.r) continue;
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float *o = out + (SECOND ? (int64_t)(col + c) * a.r + rank + i : (int64_t)(rank + i) * w.C + col + c);
+                if (*o != *o) *o = first[c][i];
+            }
+    }
+}
+
 // One block: an item's rows, 128 columns of a wide matrix, RT tiles of 16
 // ranks.  A lane loads 8 columns of 8 rows and turns them into eight fragments
 // with one permutation for every two values, so nothing is staged.  Its waves
@@ -855,16 +925,18 @@ __device__ __forceinline__ void outer_block(const LoraOuter &a, const Item &it, 
         for (int i = 0; i < RT * 8; ++i) red[0][i][lane] = __builtin_bit_cast(v4u, acc[i >> 3][i & 7]);
     }
     __syncthreads();
-    if (wave != 0 || !in) return;
+    if (wave != 0) return;
     const int64_t size = (int64_t)a.r * w.C;
     float *out = it.slot < 0 ? w.out + it.e * size : w.part + it.slot * size;
+    bool lost = false;
 #pragma unroll
     for (int j = 0; j < RT; ++j) {
         const int rank = j0 + j * 16 + kg * 4;           // four ranks, eight columns
-        if (rank >= a.r) continue;
+        if (!in || rank >= a.r) continue;
         v4f v[8];
 #pragma unroll
         for (int c = 0; c < 8; ++c) v[c] = acc[j][c] + __builtin_bit_cast(v4f, red[0][j * 8 + c][lane]);
+        lost = lost || has_nan(v);
         if constexpr (SECOND) {                          // [C][r]
 #pragma unroll
             for (int c = 0; c < 8; ++c) *reinterpret_cast<v4f *>(out + (int64_t)(col + c) * a.r + rank) = v[c];
@@ -877,6 +949,7 @@ __device__ __forceinline__ void outer_block(const LoraOuter &a, const Item &it, 
             }
         }
     }
+    if (__builtin_expect(__ballot(lost) != 0, 0)) outer_first<RT, Wide, SECOND>(a, w, it, j0, col, in, lane, out);
 }
 
 template <int RT, class WideX>
