@@ -42,8 +42,12 @@ __device__ __forceinline__ v4f mfma(v4u a, v4u b, v4f c) {
 }
 
 // Two values as a sum of N pairs of bf16, each pair in a word, the largest
-// first.  What the rounding to bf16 takes to infinity, or was infinite, has no
-// rest.
+// first.  A finite value that bf16 would round to infinity begins with bf16's
+// largest number instead; an infinity or NaN has no rest.
+constexpr float kLargestBf16 = 0x1.FEp127f;
+__device__ __forceinline__ float in_range(float v) {
+    return __builtin_isfinite(v) ? __builtin_amdgcn_fmed3f(v, -kLargestBf16, kLargestBf16) : v;
+}
 __device__ __forceinline__ float rest_of(float v, float taken) {
     const float d = v - taken;
     return d == d ? d : 0.0f;
@@ -52,7 +56,7 @@ template <int N>
 __device__ __forceinline__ void split_pair(float v0, float v1, uint32_t (&out)[N]) {
 #pragma unroll
     for (int n = 0; n < N; ++n) {
-        out[n] = bf16x2_rne(v0, v1);
+        out[n] = n == 0 ? bf16x2_rne(in_range(v0), in_range(v1)) : bf16x2_rne(v0, v1);
         v0 = rest_of(v0, __uint_as_float(out[n] << 16));
         v1 = rest_of(v1, __uint_as_float(out[n] & 0xFFFF0000u));
     }

@@ -1,8 +1,8 @@
 """The low-rank adapters' operands at the ends of their range: infinite values
-against finite ones, and products that leave fp32's range.  The reference is the
-formula in fp64, rounded to the result's type: finite values, infinities and NaN
-have to be the same (sums of whole numbers below 2^24, or one product with a
-power of two: exact)."""
+against finite ones, sums close to fp32's largest number, and products that
+leave it.  The reference is the formula in fp64, rounded to the result's type:
+finite values, infinities and NaN have to be the same (sums of whole numbers
+below 2^24, or one product with a power of two: exact)."""
 import pytest
 import torch
 
@@ -11,6 +11,8 @@ from test_gpu_lora import _by_row, _gen, _ids, _whole
 pytestmark = pytest.mark.gpu
 
 INF = float("inf")
+BIG = (2 - 2.0 ** -7) * 2.0 ** 127              # bf16's largest number
+REST = 3 * 2.0 ** -9 * 2.0 ** 127               # BIG + REST is below fp32's largest and above what bf16 rounds to infinity
 
 
 def _same(got, want):
@@ -117,6 +119,44 @@ def test_infinite_rows(mx, T, E, r, K, N):
     _check(mx, x, a, b, d_y, ids, scales, h=h)
     h[4, 2], h[8, 0], h[9, 1] = INF, -INF, float("nan")
     d_y[5, 9], d_y[17, 0], d_y[30, 3] = 1, 2, 0
+    _check(mx, x, a, b, d_y, ids, scales, h=h)
+
+
+@pytest.mark.parametrize("T,E,r,K,N", SHAPES)
+def test_sums_next_to_the_largest_number(mx, T, E, r, K, N):
+    """A x and S above what bf16 rounds to infinity, times powers of two that bring them back, or past fp32's range"""
+    ids = _ids(T, E, T)
+    x, a = torch.zeros((T, K), device="cuda"), torch.zeros((E, r, K), device="cuda")
+    b, d_y = torch.zeros((E, N, r), device="cuda"), torch.zeros((T, N), device="cuda")
+    sign = torch.where(torch.arange(T, device="cuda") % 3 == 0, -1.0, 1.0)
+    x[:, 0], x[:, 33] = sign * BIG, sign * REST
+    a[:, 1::2, 0] = a[:, 1::2, 33] = 1
+    n = torch.arange(N, device="cuda")
+    b[:, n, (2 * n + 1) % r] = 2.0 ** -60
+    b[:, 3, 1] = 4                                          # past fp32
+    d_y[:, 0], d_y[:, 2] = sign * BIG, sign * REST
+    scales = torch.ones(E, device="cuda")
+    x, a, b, d_y = (t.to(torch.bfloat16) for t in (x, a, b, d_y))
+    tables = mx.route_tables(ids.view(-1, 1), E)
+    y, hidden, _, _, _ = _formula(x, a, b, d_y, ids, scales)
+    assert float(hidden.abs().max()) == BIG + REST
+    for dtype in (torch.bfloat16, torch.float32):
+        got = torch.zeros((T, N), dtype=dtype, device="cuda")
+        kept = mx.lora_add_(got, x, a, b, tables, scales, keep_hidden=True)
+        assert _same(kept, _by_row(hidden, tables.row_token.cpu())) and _same(got, y)
+    # S = d_y b: one row of d_x each, one row for each entry of d_a
+    b, x, a = torch.zeros_like(b), torch.zeros_like(x), torch.zeros_like(a)
+    b[:, 0, 2], b[:, 2, 2] = 1, 1
+    a[:, 2, 5], a[:, 2, 6] = 2.0 ** -60, 4
+    t = torch.arange(T, device="cuda")
+    x[t, t % K] = torch.where(t < K, 2.0 ** -30, 0.0).to(torch.bfloat16)
+    h = torch.zeros((T, r), device="cuda")
+    h[0] = (2 - 2.0 ** -23) * 2.0 ** 127
+    h[7, 3] = -h[0, 0]
+    d_y[:, 10:] = 0
+    d_y[0, 10], d_y[7, 11] = 2.0 ** -30, 2.0 ** -90
+    d_y[1:, :3] = torch.where(torch.arange(T - 1, device="cuda").unsqueeze(1) < K - 1, d_y[1:, :3].float(), 0.0).to(torch.bfloat16)
+    ids[0] = ids[7] = 0
     _check(mx, x, a, b, d_y, ids, scales, h=h)
 
 
