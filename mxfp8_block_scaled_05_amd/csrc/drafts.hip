@@ -16,10 +16,14 @@
 //
 // Bounds.  A term's exponent carries three roundings of |u| 2^-24 (distance,
 // scale, product), u its distance from the maximum in powers of two.  Averaged
-// over a row |u| is at most log2 V, so a row's sum, whose groups of 32 terms
-// are added in fp64, is within 31 * 3 * ln 2 * 2^-24 + 2^-21 < 2^-17 of its
-// value (2^-18 at 2^17 columns).  A single term of |u| <= 126 is within
-// 126 * 3 * ln 2 * 2^-24 + 2^-22 < 2^-15.9; below it is 0.
+// over a row |u| is at most log2 V, so the terms of a row's sum, whose groups of
+// 32 are added in fp64, are off by 31 * 3 * ln 2 * 2^-24 + 2^-21 < 2^-17.8 of it.
+// Where a maximum rises, the sum so far is scaled by an exponential that is off
+// by 2^-23 at most, whatever the rise (the errors of rises too small for it all
+// have one sign).  A slice of kSlice columns has 64 groups of 4096 fp32 columns
+// at most, 4 at its end and 2 joins, 70 * 2^-23 < 2^-16.8; slices are joined in
+// fp64.  Together a row's sum is within 2^-16.2 of its value.  A single term of
+// |u| <= 126 is within 126 * 3 * ln 2 * 2^-24 + 2^-22 < 2^-15.9; below it is 0.
 #include <type_traits>
 
 #include "mx_launch.hpp"
@@ -33,7 +37,8 @@ constexpr int kBlock = 256;
 constexpr int kUnroll = 4;
 constexpr int kDrawBlocks = 4;              // of the race resident on a compute unit
 constexpr float kLowest = -3.402823466e38f;
-constexpr float kDrawSlack = 0x1p-15f;      // of p and q as the race sees them
+constexpr int64_t kSlice = 1 << 18;         // columns of a slice at most
+constexpr float kDrawSlack = 0x1p-15f;      // of p and q as the race sees them: a term and the row's sum
 constexpr double kStandSlack = 0x1p-16;     // of p(x) and u q(x): their terms in fp64, the rows' sums as above
 
 // A row's largest logit and the sum of e^((x - m) / temp).
@@ -573,11 +578,13 @@ void start(const DraftArgs &a, int cus, hipStream_t stream) {
 }  // namespace
 
 DraftCut draft_cut(int64_t rows, int64_t B, int64_t V, int cus) {
-    // slices of a row: one where the rows alone give every compute unit a block, else enough for four blocks each
-    int64_t slices = 1;
+    // slices of a row: as few as kSlice allows where the rows alone give every compute unit a block, else enough for four
+    // blocks each
+    int64_t slices = ceil_div(V, kSlice);
     if (rows < cus) {
         const int64_t want = ceil_div((int64_t)cus * 4, rows), most = ceil_div(V, 4096);
-        slices = want < most ? want : most;
+        const int64_t few = want < most ? want : most;
+        slices = few > slices ? few : slices;
     }
     // cuts of a race: as many blocks as are resident at once, of at least 2048 columns
     const int64_t want = B < kDrawBlocks * (int64_t)cus ? kDrawBlocks * (int64_t)cus / B : 1, most = ceil_div(V, 2048);
