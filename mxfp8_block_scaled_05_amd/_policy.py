@@ -11,6 +11,15 @@ from ._tokens import ERR_SHAPE, need, need_rows, same_device, stream_of  # noqa:
 
 _ready = None
 
+_count = getattr(torch._C, "_increment_version", None) or torch.autograd.graph.increment_version
+
+
+def written(t: torch.Tensor) -> None:
+    """The call has changed t through its address.  Autograd, which sees only
+    torch's own operations, learns it from the version counter and raises its
+    usual error where it still needs the former values."""
+    _count((t,))
+
 
 def policy_lib():
     """The library with these calls' signatures set."""

@@ -11,7 +11,7 @@ from __future__ import annotations
 import torch
 
 from . import PackedWeight, _check, packed_bytes
-from ._policy import ERR_SHAPE, need, need_bf16_rows, need_rows, policy_lib, same_device, stream_of
+from ._policy import ERR_SHAPE, need, need_bf16_rows, need_rows, policy_lib, same_device, stream_of, written
 
 _BF16, _CANONICAL, _PACKED = 0, 1, 2
 
@@ -58,6 +58,7 @@ def lora_add_(y: torch.Tensor, x: torch.Tensor, a: torch.Tensor, b: torch.Tensor
     _check(L.mxfp8_lora_add(y.data_ptr(), code, ld_y, x.data_ptr(), ld_x, T, pa, pb, ps, E, r, K, N, po, pr, rows,
                             hidden.data_ptr() if keep_hidden else None, ws.data_ptr(), need_ws, stream_of(dev)),
            "mxfp8_lora_add")
+    written(y)
     return hidden
 
 
@@ -113,4 +114,6 @@ def lora_backward_(d_x: torch.Tensor | None, d_y: torch.Tensor, x, a: torch.Tens
     _check(L.mxfp8_lora_backward(d_x.data_ptr() if d_x is not None else None, ld_dx, d_y.data_ptr(), ld_dy, px, pxs, form,
                                  ld_x, T, pa, pb, ps, E, r, K, N, po, pr, rows, ph, d_a.data_ptr(), d_b.data_ptr(),
                                  ws.data_ptr(), need_ws, stream_of(dev)), "mxfp8_lora_backward")
+    if d_x is not None:
+        written(d_x)
     return d_a, d_b
