@@ -7,11 +7,20 @@ import ctypes
 import torch
 
 from . import lib
-from ._tokens import ERR_SHAPE, need, need_rows, same_device, stream_of  # noqa: F401
+from ._tokens import ERR_SHAPE, need, need_rows, same_device, stream_of as _stream_of  # noqa: F401
 
 _ready = None
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 _count = getattr(torch._C, "_increment_version", None) or torch.autograd.graph.increment_version
+
+
+def stream_of(device: int) -> int:
+    """The current stream of the tensors' device, which has to be the current
+    one: the calls launch there, whatever device their addresses belong to."""
+    if device != _current_device():
+        raise ValueError("the tensors are on cuda:%d, but the current device is cuda:%d" % (device, _current_device()))
+    return _stream_of(device)
 
 
 def written(t: torch.Tensor) -> None:
