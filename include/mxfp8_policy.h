@@ -162,13 +162,15 @@ size_t mxfp8_verify_drafts_workspace_bytes(int64_t R, int64_t B, int64_t V, int 
  * probability w / sum w.  Where p exceeds q nowhere (rounding, or a draft row
  * without a distribution), w = p.  The decisions are those of probabilities
  * held in fp64 (close ones are taken again in fp64), with noise of 2^-32 to
- * 2^32.  A temperature near 0 (2^-60) with draft_logits NULL compares with the
+ * 2^32; a request with a close one, and every request of more than 31 drafted
+ * tokens, takes several times as long.  A temperature near 0 (2^-60) with draft_logits NULL compares with the
  * largest logit: greedy verification.
  *
  *   accepted [B] int32 : drafted tokens that stand
  *   tokens   [R] int64 : by row: the drafted tokens that stand, the next one,
  *     then -1
- *   logprobs [R] FP32  : log p of those tokens, 0 behind them
+ *   logprobs [R] FP32  : log p of those tokens, within 2^-16 and FP32's rounding;
+ *     0 behind them
  * A row without a distribution (a NaN or +Inf in it, or nothing above -Inf)
  * lets no draft stand and gives no token: -1, log-probability NaN.  A drafted
  * token outside [0, V) does not stand.

@@ -23,7 +23,8 @@
 // The parts of a finite P may be 0 or differ in sign, so against an infinity, or
 // where a product leaves fp32, they make a NaN of what is an infinity.  The
 // first part alone, which has P's sign and is 0 only with it, decides there: a
-// NaN among the sums has its tile's products taken again with that part.
+// NaN among the sums has its tile's products taken again with that part (the
+// gradients of 8192 rows with an infinity in x, d_y or b 178 to 194 us for 99).
 #include <type_traits>
 
 #include "mx_launch.hpp"
@@ -282,6 +283,8 @@ struct Tile {
 // 16 rows, 16 cache lines for 256 bytes).  The next columns' y and B are asked
 // for before the current ones are used.  Joining P once for many columns
 // matters: 8192 rows of rank 64 to 6144 take 60 us with P joined for every 256.
+// Whole calls with inputs that change: 8192 rows of rank 128, 4096 to 6144, 105 us
+// with bf16 y and 139 with fp32; 16384 rows of rank 64 140 and 213.
 // KT: steps of 32 ranks.  LOOP: several columns.  By itself rank 64 to 8192 x 6144
 // takes 51 us, rank 32 to 8192 x 4096 31 us; y alone, read and written in place
 // (201 MB), takes 37.4 at its best.
@@ -566,8 +569,9 @@ __global__ __launch_bounds__(kBlock, KT == 4 ? 1 : 2) void lora_expand_kernel(co
 // and its share of the columns of y.  Blocks beside each other on the same rows
 // take that product each for itself.  The sums over ranks stay in LDS (no
 // partials in memory), and eight waves join them once.  8192 rows of rank 64, 4096
-// to 6144: 55 us on one input, 73 with inputs that change (270 MB, 3.7 TB/s): a
-// compute unit's waves first all read x and then all update y.
+// to 6144: 56 us on one input, 73 with inputs that change (270 MB, 3.7 TB/s), and
+// 105 where y is fp32 (470 MB, 4.5 TB/s): a compute unit's waves first all read x
+// and then all update y.
 constexpr int kBothWaves = 8;
 template <class Y, int RT>
 __global__ __launch_bounds__(kBothWaves * 64) void lora_both_kernel(const LoraShrink s, const LoraExpand a) {
@@ -898,7 +902,9 @@ __device__ __forceinline__ void outer_first(const LoraOuter &a, const LoraWide &
 // with one permutation for every two values, so nothing is staged.  Its waves
 // take blocks of 32 rows in turn.  8192 rows of rank 32, x [4096] in 8 bits and d_y
 // [6144]: 35 to 40 us (134 MB, 3.4 TB/s), half of it vector arithmetic on the
-// values' forms; 4001 rows of rank 16, 2048 and 1536 in bf16: 12.8 us.
+// values' forms; 4001 rows of rank 16, 2048 and 1536 in bf16: 12.8 us.  x's form
+// changes little: whole gradients at rank 32 take 104.5 us with x in bf16, 104.7
+// canonical and 105.1 packed, at rank 128 206, 207 and 210.
 template <int RT, class Wide, bool SECOND>
 __device__ __forceinline__ void outer_block(const LoraOuter &a, const Item &it, int slab, int j0, int lane, int wave,
                                             v4u (&red)[2][RT * 8][64]) {
